@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "sol.h"
+#include "train.h"
 
 struct sol_rope3d {
     float2* dev;           // one allocation holding the three axis tables
@@ -206,9 +207,11 @@ sol_status sol_device_errors(uint32_t* flags, int32_t clear)
     const uint32_t staged = sol::rows_stage_device_error(clear != 0);
     const uint32_t qk = sol::qk_device_error(clear != 0);
     const uint32_t self = sol::selftest_device_error(clear != 0);
-    CHECK(rows != 0xffffffffu && staged != 0xffffffffu && qk != 0xffffffffu && self != 0xffffffffu, SOL_ERR_CUDA,
-          "reading the device error flags failed");
-    *flags = rows | staged | qk | self | ((sol::gemm_device_error(clear != 0) & 0xffu) << 8);
+    const uint32_t ffn = sol::ffn_device_error(clear != 0);
+    CHECK(rows != 0xffffffffu && staged != 0xffffffffu && qk != 0xffffffffu && self != 0xffffffffu &&
+              ffn != 0xffffffffu,
+          SOL_ERR_CUDA, "reading the device error flags failed");
+    *flags = rows | staged | qk | self | ((sol::gemm_device_error(clear != 0) & 0xffu) << 8) | ((ffn & 0xffu) << 16);
     return SOL_OK;
 }
 

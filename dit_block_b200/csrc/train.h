@@ -1,0 +1,79 @@
+// train.h -- host-side launchers of the training kernels (internal to the library).
+// Arguments reach these only after sol_train.cu validated them.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sol_train.h"
+
+namespace sol {
+
+// ---- gated feed-forward block (k_ffn.cu)
+
+// One matrix operand as it lies in memory: `rows` rows of `cols` bf16, row stride ld.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+// What a product's epilogue does with the accumulator.
+enum FfnEpi {
+    FFN_STORE = 0,  // out = acc (bf16 or f32; optionally added to what out holds)
+    FFN_UP = 1,     // acc = [a | b]: act = silu(a) * b, u = [a | b] if kept
+    FFN_DACT = 2,   // acc = d_act, with u = [a | b]: du, act
+};
+
+struct FfnProduct {
+    FfnEpi epi;
+    int64_t M, N, K;   // FFN_UP: N = inner (2 * inner rows of B)
+    Mat a, b;
+    bool a_mn, b_mn;   // operand stored with M (N) contiguous instead of K
+    void* out;         // FFN_STORE: the product; FFN_UP, FFN_DACT: act (FFN_DACT: may be NULL)
+    int64_t ld_out;
+    bool out_f32, accumulate;
+    void* u;           // FFN_UP: kept u or NULL; FFN_DACT: u (read)
+    int64_t ld_u;
+    void* du;          // FFN_DACT
+    int64_t ld_du;
+    float* partial;    // workspace of ffn_partial_bytes
+};
+
+// Bytes of f32 partial sums the product needs (0 where its inner dimension is not split).
+size_t ffn_partial_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K);
+cudaError_t launch_ffn_product(const FfnProduct& g, cudaStream_t s);
+// Error flags raised by these kernels' bounded waits; optionally cleared.  Synchronous.
+uint32_t ffn_device_error(bool clear);
+
+// ---- AdamW (k_adamw.cu)
+
+constexpr int kAdamwChunk = 4096;  // values of one CTA, a multiple of SOL_ADAMW_BLOCK
+
+struct AdamwTensor {
+    float* p;
+    void* copy;
+    const void* g;
+    void *m, *v;
+    float *ms, *vs;
+    int64_t n;
+    float wd;
+    uint32_t ordinal;  // place in the plan, for the rounding hash
+};
+struct AdamwChunk {
+    int32_t tensor;
+    int32_t index;     // chunk inside the tensor
+};
+struct AdamwTable {
+    const AdamwTensor* tensors;
+    const AdamwChunk* chunks;
+    int64_t n_chunks;
+};
+
+cudaError_t launch_adamw_step(const AdamwTable& t, sol_dtype grad_dt, int state_bits, const sol_adamw_scalars& h,
+                              cudaStream_t s);
+cudaError_t launch_adamw_grad_norm(float* out, const AdamwTable& t, sol_dtype grad_dt, float max_norm, void* workspace,
+                                   cudaStream_t s);
+cudaError_t launch_adamw_decode(void* m_out, void* v_out, sol_dtype out_dt, const void* m, const void* v,
+                                const float* ms, const float* vs, int64_t n, cudaStream_t s);
+
+}  // namespace sol

@@ -95,7 +95,9 @@ int32_t sol_abi_version(void);
  * bit 1 = a QK RMSNorm + RoPE kernel's bounded wait on its own asynchronous copy gave up;
  * bit 2 = sol_selftest_wait_timeout's wait gave up (as it is meant to);
  * bits 8..15 = a linear-layer kernel (sol_linear*, sol_adaln_*) gave up a bounded wait
- * in its copy / MMA / epilogue / transform pipeline.  The kernel recorded it, drained
+ * in its copy / MMA / epilogue / transform pipeline;
+ * bits 16..23 = the same for the feed-forward kernels of sol_train.h.
+ * The kernel recorded it, drained
  * its own copies and MMAs, stopped early and left its outputs incomplete.  Synchronises
  * the current device first; clear != 0 resets the flags.  Never set in normal
  * operation. */
