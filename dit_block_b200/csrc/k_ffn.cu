@@ -16,9 +16,14 @@
 // Everything outside a tensor is read as zero by the tensor copies (ragged M, N and K) and
 // never stored.
 //
-// Few tiles, long K: the K range is cut into `splits` and every (tile, split) is a work
-// item; partial sums go to an f32 workspace and k_join adds them in a fixed order and
-// applies the epilogue (see plan()).
+// The tiles that do not fill a last round of the persistent workers would leave most of them
+// idle for a whole tile: their K ranges are instead laid end to end and cut into equal pieces,
+// one a worker (see plan()).  A piece that is not a whole tile goes to an f32 slot of the
+// workspace; k_join adds the pieces of a tile in the order of K and applies the epilogue.
+//
+// The kernels of one call are launched so that the next one's set-up overlaps the last one's
+// end (programmatic dependent launch); every thread waits for the end of the kernel before
+// (griddep_wait) ahead of its first access to global memory.
 //
 // Warp roles: 0 copies, 1 issues MMAs into one of two TMEM accumulators, the others are the
 // epilogue.  Every wait is bounded; one that gives up raises an error flag and the CTA
@@ -52,7 +57,7 @@ constexpr uint32_t kWaitLimit = 4096;      // polls of <= ~1 ms each
 constexpr uint32_t kPollLimit = 1u << 26;  // polls without a suspend hint
 constexpr int B200_SMS = 148;              // plan() is a function of the sizes alone
 
-enum Mode : int { STORE = FFN_STORE, UP = FFN_UP, DACT = FFN_DACT, PART = 3 };
+enum Mode : int { STORE = FFN_STORE, UP = FFN_UP, DACT = FFN_DACT };
 
 template <bool PAIR> __host__ __device__ constexpr int tile_m() { return PAIR ? 2 * BM : BM; }
 template <bool PAIR> __host__ __device__ constexpr int tile_n() { return PAIR ? 256 : 128; }
@@ -75,16 +80,18 @@ __device__ uint32_t g_error;
 struct Params {
     int32_t M, N, kblocks;       // N: columns of the output (UP: inner)
     int32_t tiles_m, tiles_n;
-    int32_t splits, kb_split;    // K cut into `splits` ranges of kb_split blocks (the last may be shorter)
-    int64_t items;               // tiles_m * tiles_n * splits
+    int64_t whole, tiles;        // tiles [0, whole) are worked on whole, one after another by each worker
+    int32_t pieces, piece_kb;    // tiles [whole, tiles): their K end to end in `pieces` of piece_kb blocks
+    int32_t a_blocks, b_blocks;  // 1: a copy brings both 64-row halves of the operand (see make_map)
+    int32_t out_f32, accumulate;
+    int32_t wide;                // rows of out, u and du (and their second halves) begin on 32-byte boundaries
     void* out;
     int64_t ld_out;
-    int32_t out_f32, accumulate;
     bf16* u;
     int64_t ld_u;
     bf16* du;
     int64_t ld_du;
-    float* partial;              // [splits, M, N]
+    float* slots;                // f32 [2 * pieces, TN / 8, TM, 8]: pieces that are not whole tiles
 };
 
 // Shared-memory descriptor of an operand tile with M (N) contiguous, in boxes of 64
@@ -97,26 +104,61 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr)
            ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
-struct Item {
-    int32_t m_blk, n_blk, split, kb0, kb1;
+// A piece of work: K blocks [kb0, kb1) of a tile; slot >= 0 where they are not all of its K.
+struct Piece {
+    int32_t m_blk, n_blk, kb0, kb1;
+    int64_t slot;
 };
 
-__device__ __forceinline__ Item item_at(int64_t i, const Params& p)
+// Tile t -> its blocks of rows and columns, in groups of GROUP_M m-blocks so that the tiles
+// worked on at one time share rows of A and of B in L2.
+__device__ __forceinline__ void tile_at(int64_t t, const Params& p, int32_t& m_blk, int32_t& n_blk)
 {
-    Item it;
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    it.split = (int32_t)(i / tiles);
-    const int64_t t = i - it.split * tiles;
-    const int32_t per_group = GROUP_M * p.tiles_n;
+    const int64_t per_group = (int64_t)GROUP_M * p.tiles_n;
     const int32_t g = (int32_t)(t / per_group);
     const int32_t gm = min(GROUP_M, p.tiles_m - g * GROUP_M);
-    const int32_t local = (int32_t)(t - (int64_t)g * per_group);
-    it.m_blk = g * GROUP_M + local % gm;
-    it.n_blk = local / gm;
-    it.kb0 = it.split * p.kb_split;
-    it.kb1 = min(it.kb0 + p.kb_split, p.kblocks);
-    return it;
+    const int32_t local = (int32_t)(t - g * per_group);
+    m_blk = g * GROUP_M + local % gm;
+    n_blk = local / gm;
 }
+
+// The pieces of one worker, the same sequence for every role: whole tiles, then its share of
+// the streamed K range.  A share begins inside a tile (slot 0 of the worker) at most once and
+// ends inside another (slot 1) at most once.
+struct Walk {
+    int64_t t, q, end, worker;
+};
+
+__device__ __forceinline__ Walk walk_begin(int64_t worker) { return Walk{worker, 0, 0, worker}; }
+
+__device__ __forceinline__ bool walk_next(Walk& w, const Params& p, int64_t n_workers, Piece& x)
+{
+    if (w.t < p.whole) {
+        tile_at(w.t, p, x.m_blk, x.n_blk);
+        x.kb0 = 0;
+        x.kb1 = p.kblocks;
+        x.slot = -1;
+        w.t += n_workers;
+        return true;
+    }
+    if (w.q >= w.end) {
+        if (w.worker >= p.pieces) return false;
+        w.q = w.worker * p.piece_kb;
+        w.end = min(w.q + p.piece_kb, (p.tiles - p.whole) * p.kblocks);
+        w.t = p.whole + w.worker;  // from here on: the share's number
+        w.worker += n_workers;
+    }
+    const int64_t tile = w.q / p.kblocks;
+    x.kb0 = (int32_t)(w.q - tile * p.kblocks);
+    x.kb1 = (int32_t)min((int64_t)p.kblocks, x.kb0 + (w.end - w.q));
+    tile_at(p.whole + tile, p, x.m_blk, x.n_blk);
+    x.slot = x.kb0 == 0 && x.kb1 == p.kblocks ? -1 : 2 * (w.t - p.whole) + (x.kb0 == 0 ? 1 : 0);
+    w.q += x.kb1 - x.kb0;
+    return true;
+}
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 struct Where {
     uint32_t rank;
@@ -139,6 +181,22 @@ __device__ __forceinline__ void raise_abort(Bars* b, uint32_t code)
     atomicOr(&g_error, code);
 }
 
+// The 128 rows of one operand, [x0, x0 + 64) and [x1, x1 + 64), for the 64 K from k on.  One copy
+// where the map's box holds both halves, else two.
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int32_t form, int32_t x0, int32_t x1,
+                                             int32_t k, uint32_t bar, bool remote)
+{
+    if (MN && form) {
+        remote ? tc::tma_load_3d_pair(dst, map, 0, k, x0 / BOX, bar) : tc::tma_load_3d(dst, map, 0, k, x0 / BOX, bar);
+        return;
+    }
+    const int32_t c0 = MN ? x0 : k, r0 = MN ? k : x0, c1 = MN ? x1 : k, r1 = MN ? k : x1;
+    remote ? tc::tma_load_2d_pair(dst, map, c0, r0, bar) : tc::tma_load_2d(dst, map, c0, r0, bar);
+    if (form) return;
+    remote ? tc::tma_load_2d_pair(dst + BOX_BYTES, map, c1, r1, bar) : tc::tma_load_2d(dst + BOX_BYTES, map, c1, r1, bar);
+}
+
 // Producer (one thread per CTA): this CTA's 128 rows of A and its 128 rows of B (64 of the
 // gated half and 64 of the other for UP in the single shape; in a pair the leader loads the
 // gated half, the peer the other).  The peer's copies complete on the leader's barrier,
@@ -153,8 +211,9 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
     int32_t last[STAGES];
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) last[i] = -1;
-    for (int64_t i = w.worker; i < p.items && !b->abort; i += w.n_workers) {
-        const Item it = item_at(i, p);
+    Walk walk = walk_begin(w.worker);
+    Piece it;
+    while (!b->abort && walk_next(walk, p, w.n_workers, it)) {
         const int32_t ma = it.m_blk * tile_m<PAIR>() + (int32_t)w.rank * BM;
         int32_t n0, n1;
         if (MODE == UP) {
@@ -175,24 +234,13 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
                 break;
             }
             const uint32_t dst = smem_u32(ring + (size_t)s * STAGE_BYTES);
-            const int32_t k = kb * BK;
             uint32_t bar = smem_u32(&b->full[s]);
             if (remote)
                 bar = tc::mapa(bar, 0);
             else
                 mbar_arrive_expect_tx(bar, PAIR ? 2 * STAGE_BYTES : STAGE_BYTES);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int32_t m = ma + h * BOX, n = h ? n1 : n0;
-                const uint32_t da = dst + h * BOX_BYTES, db = dst + OP_BYTES + h * BOX_BYTES;
-                if (remote) {
-                    tc::tma_load_2d_pair(da, tmA, A_MN ? m : k, A_MN ? k : m, bar);
-                    tc::tma_load_2d_pair(db, tmB, B_MN ? n : k, B_MN ? k : n, bar);
-                } else {
-                    tc::tma_load_2d(da, tmA, A_MN ? m : k, A_MN ? k : m, bar);
-                    tc::tma_load_2d(db, tmB, B_MN ? n : k, B_MN ? k : n, bar);
-                }
-            }
+            load_operand<A_MN>(dst, tmA, p.a_blocks, ma, ma + BOX, kb * BK, bar, remote);
+            load_operand<B_MN>(dst + OP_BYTES, tmB, p.b_blocks, n0, n1, kb * BK, bar, remote);
             last[s] = (int32_t)phase;
             if (++s == STAGES) {
                 s = 0;
@@ -224,8 +272,9 @@ __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
     int s = 0;
     uint32_t phase = 0;
     int64_t n = 0;
-    for (int64_t i = w.worker; i < p.items && !b->abort; i += w.n_workers, ++n) {
-        const Item it = item_at(i, p);
+    Walk walk = walk_begin(w.worker);
+    Piece it;
+    for (; !b->abort && walk_next(walk, p, w.n_workers, it); ++n) {
         const int ab = (int)(n & 1);
         if (!wait_or_abort<PAIR>(smem_u32(&b->acc_empty[ab]), (uint32_t)((n >> 1) & 1) ^ 1u, b)) {
             raise_abort(b, 4u);
@@ -302,14 +351,73 @@ __device__ __forceinline__ void dact_one(float& d, float& a, float& b)
     b = db;
 }
 
-// Eight output values of one row from column `col` on: to bf16 or f32, optionally added to
-// what is there.
-__device__ __forceinline__ void store8(const Params& p, int64_t row, int32_t col, float* v)
+// 32 bytes in one instruction (both on a 32-byte boundary): a row-per-thread epilogue touches
+// whole 32-byte sectors with it.
+__device__ __forceinline__ void st256(void* p, const uint4& a, const uint4& b)
 {
-    if (p.out_f32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ void ld256(const void* p, uint4& a, uint4& b)
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p)
+                 : "memory");
+}
+
+// Stores the first `n` (8 or 16) of 16 bf16 values.
+__device__ __forceinline__ void put16(bf16* dst, const float* v, int n, int wide)
+{
+    const uint4 lo = pack<bf16>(v), hi = pack<bf16>(v + 8);
+    if (wide && n == 16) {
+        st256(dst, lo, hi);
+    } else {
+        *reinterpret_cast<uint4*>(dst) = lo;
+        if (n == 16) *reinterpret_cast<uint4*>(dst + 8) = hi;
+    }
+}
+__device__ __forceinline__ void get16(const bf16* src, uint4& lo, uint4& hi, int n, int wide)
+{
+    if (wide && n == 16) {
+        ld256(src, lo, hi);
+    } else {
+        lo = ld_plain(src);
+        hi = n == 16 ? ld_plain(src + 8) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// The epilogue of 16 columns of one row, the first n of them inside the output.  STORE: v is
+// the product.  UP: v and g are a and b.  DACT: v is d_act, ua and ub hold a and b.
+template <int MODE>
+__device__ __forceinline__ void finish16(const Params& p, int64_t row, int32_t col, int n, float* v, const float* g,
+                                         const uint4* ua, const uint4* ub)
+{
+    if constexpr (MODE == UP) {
+        if (p.u) {
+            put16(p.u + row * p.ld_u + col, v, n, p.wide);
+            put16(p.u + row * p.ld_u + p.N + col, g, n, p.wide);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = v[e] * sigmoid_fast(v[e]) * g[e];
+        put16(static_cast<bf16*>(p.out) + row * p.ld_out + col, v, n, p.wide);
+    } else if constexpr (MODE == DACT) {
+        float a[16], b[16];
+        unpack<bf16>(ua[0], a);
+        unpack<bf16>(ua[1], a + 8);
+        unpack<bf16>(ub[0], b);
+        unpack<bf16>(ub[1], b + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dact_one(v[e], a[e], b[e]);
+        put16(p.du + row * p.ld_du + col, a, n, p.wide);
+        put16(p.du + row * p.ld_du + p.N + col, b, n, p.wide);
+        if (p.out) put16(static_cast<bf16*>(p.out) + row * p.ld_out + col, v, n, p.wide);
+    } else if (p.out_f32) {
         float* dst = static_cast<float*>(p.out) + row * p.ld_out + col;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
+            if (4 * h >= n) break;
             float4* q = reinterpret_cast<float4*>(dst + 4 * h);
             float4 x = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
             if (p.accumulate) {
@@ -320,52 +428,35 @@ __device__ __forceinline__ void store8(const Params& p, int64_t row, int32_t col
         }
     } else {
         bf16* dst = static_cast<bf16*>(p.out) + row * p.ld_out + col;
-        if (p.accumulate) {
-            float o[8];
-            unpack<bf16>(ld_plain(dst), o);
+        if (p.accumulate) {  // added in fp32, rounded once
+            uint4 lo, hi;
+            get16(dst, lo, hi, n, p.wide);
+            float o[16];
+            unpack<bf16>(lo, o);
+            unpack<bf16>(hi, o + 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += o[e];
+            for (int e = 0; e < 16; ++e) v[e] += o[e];
         }
-        *reinterpret_cast<uint4*>(dst) = pack<bf16>(v);
+        put16(dst, v, n, p.wide);
     }
 }
 
-// act (and u) of eight columns
-__device__ __forceinline__ void up8(const Params& p, int64_t row, int32_t col, float* a, const float* b)
-{
-    if (p.u) {
-        *reinterpret_cast<uint4*>(p.u + row * p.ld_u + col) = pack<bf16>(a);
-        *reinterpret_cast<uint4*>(p.u + row * p.ld_u + p.N + col) = pack<bf16>(b);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = a[e] * sigmoid_fast(a[e]) * b[e];
-    *reinterpret_cast<uint4*>(static_cast<bf16*>(p.out) + row * p.ld_out + col) = pack<bf16>(a);
-}
-
-// du and act of eight columns from d_act and the loaded a and b
-__device__ __forceinline__ void dact8(const Params& p, int64_t row, int32_t col, float* d, const uint4& ua,
-                                      const uint4& ub)
-{
-    float a[8], b[8];
-    unpack<bf16>(ua, a);
-    unpack<bf16>(ub, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dact_one(d[e], a[e], b[e]);
-    *reinterpret_cast<uint4*>(p.du + row * p.ld_du + col) = pack<bf16>(a);
-    *reinterpret_cast<uint4*>(p.du + row * p.ld_du + p.N + col) = pack<bf16>(b);
-    if (p.out) *reinterpret_cast<uint4*>(static_cast<bf16*>(p.out) + row * p.ld_out + col) = pack<bf16>(d);
-}
+// Columns of [col, col + 16) inside a width of N (a multiple of 8).
+__device__ __forceinline__ int inside(int32_t col, int32_t N) { return min(max(N - col, 0), 16); }
 
 // Epilogue: thread (warp w, lane l) owns accumulator row 32 * (w % 4) + l of this CTA and,
 // with eight warps, half of its columns.
 template <int MODE, bool PAIR> __device__ void run_epilogue(const Params& p, Bars* b, const Where& w)
 {
-    constexpr int EW = epi_warps(MODE), H = EW / 4, TN = tile_n<PAIR>();
+    constexpr int EW = epi_warps(MODE), H = EW / 4, TN = tile_n<PAIR>(), TM = tile_m<PAIR>();
+    constexpr int WIDTH = MODE == UP ? TN / 2 : TN;  // UP: a in columns [0, WIDTH), b behind them
+    constexpr int CH = WIDTH / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, part = (warp - EPI_WARP0) / 4;
     int64_t n = 0;
-    for (int64_t i = w.worker; i < p.items; i += w.n_workers, ++n) {
-        const Item it = item_at(i, p);
+    Walk walk = walk_begin(w.worker);
+    Piece it;
+    for (; walk_next(walk, p, w.n_workers, it); ++n) {
         const int ab = (int)(n & 1);
         const bool got = wait_or_abort<PAIR>(smem_u32(&b->acc_full[ab]), (uint32_t)((n >> 1) & 1), b);
         if (!__all_sync(0xffffffffu, got)) {
@@ -373,54 +464,44 @@ template <int MODE, bool PAIR> __device__ void run_epilogue(const Params& p, Bar
             break;
         }
         tc::fence_after_sync();
-        const int64_t row = (int64_t)it.m_blk * tile_m<PAIR>() + (int64_t)w.rank * BM + quarter * 32 + lane;
+        const int tile_row = (int)w.rank * BM + quarter * 32 + lane;
+        const int64_t row = (int64_t)it.m_blk * TM + tile_row;
         const bool live = row < p.M;
         const uint32_t t = b->tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ab * TN);
-        float v[32];
-        if constexpr (MODE == UP) {
-            constexpr int HALF = TN / 2, CH = HALF / 32;  // a in columns [0, HALF), b behind them
-            float g[32];
+        float v[32], g[MODE == UP ? 32 : 1];
 #pragma unroll 1
-            for (int c = part * (CH / H); c < (part + 1) * (CH / H); ++c) {
-                const int32_t col = it.n_blk * HALF + 32 * c;
-                tc::ld32(t + 32 * c, v);
-                tc::ld32(t + HALF + 32 * c, g);
-                if (!live) continue;
+        for (int c = part * (CH / H); c < (part + 1) * (CH / H); ++c) {
+            const int32_t col = it.n_blk * WIDTH + 32 * c;
+            const int n0 = inside(col, p.N), n1 = inside(col + 16, p.N);
+            uint4 ua[4], ub[4];
+            if (MODE == DACT && live && it.slot < 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = h ? n1 : n0;
+                    if (!k) break;
+                    get16(p.u + row * p.ld_u + col + 16 * h, ua[2 * h], ua[2 * h + 1], k, p.wide);
+                    get16(p.u + row * p.ld_u + p.N + col + 16 * h, ub[2 * h], ub[2 * h + 1], k, p.wide);
+                }
+            }
+            tc::ld32(t + 32 * c, v);
+            if constexpr (MODE == UP) tc::ld32(t + WIDTH + 32 * c, g);
+            if (!live) continue;
+            if (it.slot >= 0) {
+                // [column group of 8][row][8]: a warp's 32 rows are 1 KiB in a row
+                float* q = p.slots + ((it.slot * (TN / 8) + 4 * c) * TM + tile_row) * 8;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (col + 8 * j < p.N) up8(p, row, col + 8 * j, v + 8 * j, g + 8 * j);
-            }
-        } else {
-            constexpr int CH = TN / 32;
-#pragma unroll 1
-            for (int c = part * (CH / H); c < (part + 1) * (CH / H); ++c) {
-                const int32_t col = it.n_blk * TN + 32 * c;
-                uint4 ua[4], ub[4];
-                if constexpr (MODE == DACT) {
+                    st256(q + j * TM * 8, *reinterpret_cast<uint4*>(v + 8 * j), *reinterpret_cast<uint4*>(v + 8 * j + 4));
+                if constexpr (MODE == UP) {
+                    q += (WIDTH / 8) * TM * 8;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (live && col + 8 * j < p.N) {
-                            ua[j] = ld_stream_ro(p.u + row * p.ld_u + col + 8 * j);
-                            ub[j] = ld_stream_ro(p.u + row * p.ld_u + p.N + col + 8 * j);
-                        }
+                        st256(q + j * TM * 8, *reinterpret_cast<uint4*>(g + 8 * j), *reinterpret_cast<uint4*>(g + 8 * j + 4));
                 }
-                tc::ld32(t + 32 * c, v);
-                if (!live) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (col + 8 * j >= p.N) continue;
-                    if constexpr (MODE == DACT) {
-                        dact8(p, row, col + 8 * j, v + 8 * j, ua[j], ub[j]);
-                    } else if constexpr (MODE == STORE) {
-                        store8(p, row, col + 8 * j, v + 8 * j);
-                    } else {
-                        float4* q = reinterpret_cast<float4*>(p.partial + ((int64_t)it.split * p.M + row) * p.N + col +
-                                                              8 * j);
-                        q[0] = make_float4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
-                        q[1] = make_float4(v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]);
-                    }
-                }
+                continue;
             }
+            if (n0) finish16<MODE>(p, row, col, n0, v, g, ua, ub);
+            if (n1) finish16<MODE>(p, row, col + 16, n1, v + 16, g + (MODE == UP ? 16 : 0), ua + 2, ub + 2);
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -481,6 +562,8 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
     if constexpr (PAIR) tc::cluster_sync();  // both CTAs' barriers exist before any remote arrival
     tc::fence_after_sync();
 
+    griddep_launch();
+    griddep_wait();
     if (warp == 0) {
         if (lane == 0) run_producer<MODE, A_MN, B_MN, PAIR>(&tmA, &tmB, p, ring, b, w);
     } else if (warp == 1) {
@@ -512,36 +595,56 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
     }
 }
 
-// Adds the partial sums of a split product in the order of the splits and applies its
-// epilogue; eight columns a thread.  UP: the partials hold [a | b] (2 * N columns).
-template <int MODE> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
+// Adds the pieces of the streamed tiles in the order of K and applies the epilogue.  One tile
+// a blockIdx.y; a warp takes 4 rows x 8 groups of 16 columns, so that slots are read in runs
+// of 128 bytes and rows are written in runs of 256.
+template <int MODE, bool PAIR> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
-    const int64_t per_row = p.N / 8, total = (int64_t)p.M * per_row;
-    const int64_t width = MODE == UP ? 2 * (int64_t)p.N : p.N, plane = (int64_t)p.M * width;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = i / per_row;
-        const int32_t col = (int32_t)(i - row * per_row) * 8;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const float* q = p.partial + row * width + col;
-        for (int s = 0; s < p.splits; ++s, q += plane) {
-            float f[8];
-            unpack<float>(ld_stream(q), f);
-            unpack<float>(ld_stream(q + 4), f + 4);
+    constexpr int TM = tile_m<PAIR>(), TN = tile_n<PAIR>(), WIDTH = MODE == UP ? TN / 2 : TN, GROUPS = WIDTH / 16;
+    griddep_launch();
+    griddep_wait();
+    const int64_t first = (int64_t)blockIdx.y * p.kblocks, last = first + p.kblocks;  // this tile's K in the range
+    const int64_t w0 = first / p.piece_kb, w1 = (last - 1) / p.piece_kb;
+    if (w0 == w1) return;  // the whole tile was one worker's
+    int32_t m_blk, n_blk;
+    tile_at(p.whole + blockIdx.y, p, m_blk, n_blk);
+    const int rows = (int)min((int64_t)TM, (int64_t)p.M - (int64_t)m_blk * TM);
+    const int lane = threadIdx.x & 31;
+    constexpr int ACROSS = GROUPS < 8 ? GROUPS : 8, STEPS = GROUPS / ACROSS;
+    for (int i = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < (rows + 3) / 4 * STEPS;
+         i += gridDim.x * blockDim.x >> 5) {
+        if (lane >= 4 * ACROSS) break;
+        const int r = (i / STEPS) * 4 + (lane & 3), c = (i % STEPS) * ACROSS + (lane >> 2);
+        const int64_t row = (int64_t)m_blk * TM + r;
+        const int32_t col = n_blk * WIDTH + 16 * c;
+        const int n = inside(col, p.N);
+        if (r >= rows || n == 0) continue;
+        float v[16] = {}, g[16] = {};
+        for (int64_t w = w0; w <= w1; ++w) {
+            const int64_t slot = 2 * w + (w * p.piece_kb <= first ? 1 : 0);
+            const float* q = p.slots + ((slot * (TN / 8) + 2 * c) * TM + r) * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += f[e];
-            if constexpr (MODE == UP) {
-                unpack<float>(ld_stream(q + p.N), f);
-                unpack<float>(ld_stream(q + p.N + 4), f + 4);
+            for (int j = 0; j < 2; ++j) {
+                float f[8];
+                unpack<float>(ld_plain(q + j * TM * 8), f);
+                unpack<float>(ld_plain(q + j * TM * 8 + 4), f + 4);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] += f[e];
+                for (int e = 0; e < 8; ++e) v[8 * j + e] += f[e];
+                if constexpr (MODE == UP) {
+                    const float* qb = q + (WIDTH / 8 + j) * TM * 8;
+                    unpack<float>(ld_plain(qb), f);
+                    unpack<float>(ld_plain(qb + 4), f + 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[8 * j + e] += f[e];
+                }
             }
         }
-        if constexpr (MODE == UP)
-            up8(p, row, col, v, g);
-        else if constexpr (MODE == DACT)
-            dact8(p, row, col, v, ld_stream_ro(p.u + row * p.ld_u + col), ld_stream_ro(p.u + row * p.ld_u + p.N + col));
-        else
-            store8(p, row, col, v);
+        uint4 ua[2], ub[2];
+        if constexpr (MODE == DACT) {
+            get16(p.u + row * p.ld_u + col, ua[0], ua[1], n, p.wide);
+            get16(p.u + row * p.ld_u + p.N + col, ub[0], ub[1], n, p.wide);
+        }
+        finish16<MODE>(p, row, col, n, v, g, ua, ub);
     }
 }
 
@@ -566,58 +669,63 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// Boxes of 64 x 64 in the 128-byte swizzle; what lies outside the tensor reads as zero.
-bool make_map(CUtensorMap* m, const Mat& t)
+// Tensor map of an operand in the 128-byte swizzle; what lies outside the tensor reads as zero.  Sets
+// *both where one copy brings both 64-row halves of a 128-row tile:
+//   K contiguous: boxes of 64 K x 128 rows (not where the halves are apart: `halves`);
+//   M (N) contiguous: the 64-wide column blocks as a third dimension, boxes of 64 x 64 x 2, where the width
+//   is a multiple of 64, so that no block reaches into the next row.
+bool make_map(CUtensorMap* m, const Mat& t, bool mn, bool halves, int32_t* both)
 {
     auto fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)t.cols, (cuuint64_t)t.rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)t.ld * 2};
-    const cuuint32_t box[2] = {ffn::BOX, ffn::BOX};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(t.p), dims, strides, box, estr,
+    const bool blocks = mn && t.cols % ffn::BOX == 0;
+    *both = mn ? blocks : !halves;
+    const cuuint64_t dims[3] = {(cuuint64_t)(blocks ? ffn::BOX : t.cols), (cuuint64_t)t.rows,
+                                (cuuint64_t)(t.cols / ffn::BOX)};
+    const cuuint64_t strides[2] = {(cuuint64_t)t.ld * 2, ffn::BOX * 2};
+    const cuuint32_t box[3] = {ffn::BOX, (cuuint32_t)(mn || halves ? ffn::BOX : 2 * ffn::BOX), 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, blocks ? 3 : 2, const_cast<void*>(t.p), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tile shape and K split of a product, from its sizes alone.
+// Tile shape of a product and how its last tiles are shared out, from its sizes alone.
 struct Plan {
     bool pair;
-    int32_t tiles_m, tiles_n, kblocks, splits, kb_split;
+    int32_t tiles_m, tiles_n, kblocks;
+    int64_t tiles, whole;
+    int32_t pieces, piece_kb;
 };
 
 Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 {
-    Plan r;
+    Plan r{};
     r.pair = M > ffn::BM;
-    const int64_t tm = r.pair ? 256 : 128, tn = r.pair ? 256 : 128, workers = r.pair ? ffn::B200_SMS / 2 : ffn::B200_SMS;
+    const int64_t tm = r.pair ? 256 : 128, tn = epi == FFN_UP ? tm / 2 : tm;
+    const int64_t workers = r.pair ? ffn::B200_SMS / 2 : ffn::B200_SMS;
     r.kblocks = (int32_t)((K + ffn::BK - 1) / ffn::BK);
-    // microseconds: a k-block of a tile with every worker busy, a tile's fill and drain, the
-    // f32 partials written and read at 5 TB/s, the second launch
-    const double t_kb = r.pair ? 0.44 : 0.37, t_tile = 1.0, t_join = 4.0, mb = (double)M * (double)N * 8e-6 / 5.0 *
-                                                                            (epi == FFN_UP ? 2 : 1);
-    double best = 0;
-    r.splits = 0;
-    for (int32_t want = 1; want <= 32; ++want) {
-        const int32_t kb = std::max(1, (r.kblocks + want - 1) / want), s = std::max(1, (r.kblocks + kb - 1) / kb);
-        if (s != want) continue;
-        const int64_t nt = epi == FFN_UP && s == 1 ? tn / 2 : tn, n = epi == FFN_UP && s > 1 ? 2 * N : N;
-        const int64_t tiles = ((M + tm - 1) / tm) * ((n + nt - 1) / nt);
-        const double waves = (double)((tiles * s + workers - 1) / workers);
-        const double t = waves * (kb * t_kb + t_tile) + (s > 1 ? s * mb + t_join : 0.0);
-        if (!r.splits || t < best) {
-            best = t;
-            r.splits = s;
-            r.kb_split = kb;
-            r.tiles_m = (int32_t)((M + tm - 1) / tm);
-            r.tiles_n = (int32_t)((n + nt - 1) / nt);
-        }
-    }
+    r.tiles_m = (int32_t)((M + tm - 1) / tm);
+    r.tiles_n = (int32_t)((N + tn - 1) / tn);
+    r.tiles = r.whole = (int64_t)r.tiles_m * r.tiles_n;
+    const int64_t rest = r.tiles % workers, q = rest * r.kblocks;
+    if (!rest) return r;
+    // microseconds: a k-block of a tile with every worker busy; the join's launch; the pieces written
+    // and read back
+    const double t_kb = r.pair ? 0.3 : 0.35;
+    const int64_t most = std::min<int64_t>(workers, std::max<int64_t>(q / 4, 1));  // at least four k-blocks a piece
+    const int64_t kb = (q + most - 1) / most, pieces = (q + kb - 1) / kb;
+    const double area = (double)std::min(M, tm) * (double)(r.pair ? 256 : 128) * 4e-6;  // MB of a slot
+    const double join = 3.0 + 2.0 * area * (double)(pieces + rest) / 6.0;
+    if ((double)(r.kblocks - kb) * t_kb <= join) return r;
+    r.whole = r.tiles - rest;
+    r.pieces = (int32_t)pieces;
+    r.piece_kb = (int32_t)kb;
     return r;
 }
 
 template <int MODE, bool A_MN, bool B_MN, bool PAIR>
-cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ffn::Params& p, cudaStream_t s)
+cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ffn::Params& p, bool after, cudaStream_t s)
 {
     auto kern = ffn::k_product<MODE, A_MN, B_MN, PAIR>;
     constexpr int kMaxDevices = 64;
@@ -627,19 +735,19 @@ cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ff
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeClusterDimension;
-    la[0].val.clusterDim.x = 2;
-    la[0].val.clusterDim.y = 1;
-    la[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute la[2];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    la[1].id = cudaLaunchAttributeClusterDimension;
+    la[1].val.clusterDim.x = 2;
+    la[1].val.clusterDim.y = 1;
+    la[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(ffn::block_threads(MODE));
     cfg.dynamicSmemBytes = ffn::kSmemBytes;
     cfg.stream = s;
-    if (PAIR) {
-        cfg.attrs = la;
-        cfg.numAttrs = 1;
-    }
+    cfg.attrs = after ? la : la + 1;
+    cfg.numAttrs = (after ? 1 : 0) + (PAIR ? 1 : 0);
     int64_t workers;
     {
         std::lock_guard<std::mutex> lk(mu);
@@ -649,6 +757,8 @@ cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ff
             int n = sm_count();
             if (PAIR) {
                 cudaLaunchConfig_t q = cfg;
+                q.attrs = la + 1;
+                q.numAttrs = 1;
                 q.gridDim = dim3(2 * (sm_count() / 2));
                 if (cudaOccupancyMaxActiveClusters(&n, kern, &q) != cudaSuccess || n < 1) n = sm_count() / 2;
             }
@@ -656,63 +766,70 @@ cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ff
         }
         workers = workers_dev[dev];
     }
-    workers = std::min<int64_t>(p.items, workers);
+    workers = std::min<int64_t>(std::max<int64_t>(p.whole, p.pieces), workers);
     cfg.gridDim = dim3((unsigned)(PAIR ? 2 * workers : workers));
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, p);
 }
 
 template <int MODE, bool A_MN, bool B_MN>
-cudaError_t launch_shape(bool pair, const CUtensorMap& ma, const CUtensorMap& mb, const ffn::Params& p, cudaStream_t s)
+cudaError_t launch_shape(bool pair, const CUtensorMap& ma, const CUtensorMap& mb, const ffn::Params& p, bool after,
+                         cudaStream_t s)
 {
-    return pair ? launch_kernel<MODE, A_MN, B_MN, true>(ma, mb, p, s)
-                : launch_kernel<MODE, A_MN, B_MN, false>(ma, mb, p, s);
+    return pair ? launch_kernel<MODE, A_MN, B_MN, true>(ma, mb, p, after, s)
+                : launch_kernel<MODE, A_MN, B_MN, false>(ma, mb, p, after, s);
 }
 
-// The operand layouts that the block uses: K | K (forward), K | N (d_act, dx), M | N (dW).
-template <int MODE>
-cudaError_t launch_layout(bool pair, bool a_mn, bool b_mn, const CUtensorMap& ma, const CUtensorMap& mb,
-                          const ffn::Params& p, cudaStream_t s)
+template <int MODE, bool PAIR> cudaError_t launch_join(const ffn::Params& p, cudaStream_t s)
 {
-    if (a_mn && b_mn) return launch_shape<MODE, true, true>(pair, ma, mb, p, s);
-    if (!a_mn && b_mn) return launch_shape<MODE, false, true>(pair, ma, mb, p, s);
-    if (!a_mn && !b_mn) return launch_shape<MODE, false, false>(pair, ma, mb, p, s);
-    return cudaErrorInvalidValue;
+    // a warp takes 4 rows x up to 128 columns of one tile
+    const int64_t warps = (std::min<int64_t>(p.M, ffn::tile_m<PAIR>()) + 3) / 4 *
+                          std::max(1, ffn::tile_n<PAIR>() / (MODE == ffn::UP ? 256 : 128));
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)((warps + 7) / 8), (unsigned)(p.tiles - p.whole));
+    cfg.stream = s;
+    cfg.attrs = la;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ffn::k_join<MODE, PAIR>, p);
 }
 
-template <int MODE> cudaError_t launch_join(const ffn::Params& p, cudaStream_t s)
+template <int MODE> cudaError_t launch_join(bool pair, const ffn::Params& p, cudaStream_t s)
 {
-    const int64_t n = (int64_t)p.M * (p.N / 8);
-    const int64_t grid = std::min<int64_t>((n + 255) / 256, (int64_t)sm_count() * 16);
-    ffn::k_join<MODE><<<(unsigned)grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return pair ? launch_join<MODE, true>(p, s) : launch_join<MODE, false>(p, s);
 }
+
+bool on32(const void* p, int64_t ld, int64_t esz) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld * esz % 32 == 0; }
 
 }  // namespace
 
-size_t ffn_partial_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K)
+size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 {
     const Plan r = plan(epi, M, N, K);
-    return r.splits > 1 ? (size_t)r.splits * (size_t)M * (size_t)N * (epi == FFN_UP ? 8 : 4) : 0;
+    return (size_t)r.pieces * 2 * (r.pair ? 256 * 256 : 128 * 128) * 4;
 }
 
-cudaError_t launch_ffn_product(const FfnProduct& g, cudaStream_t s)
+cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
 {
-    if (g.M == 0 || g.N == 0) return cudaSuccess;
     CUtensorMap ma, mb;
-    if (!make_map(&ma, g.a) || !make_map(&mb, g.b)) {
+    const Plan r = plan(g.epi, g.M, g.N, g.K);
+    ffn::Params p{};
+    if (!make_map(&ma, g.a, g.a_mn, false, &p.a_blocks) ||
+        !make_map(&mb, g.b, g.b_mn, g.epi == FFN_UP && !r.pair, &p.b_blocks)) {
         record_error("tensor map encoding failed (cuTensorMapEncodeTiled unavailable or refused the layout)");
         return cudaErrorInvalidValue;
     }
-    const Plan r = plan(g.epi, g.M, g.N, g.K);
-    ffn::Params p{};
     p.M = (int32_t)g.M;
     p.N = (int32_t)g.N;
     p.kblocks = r.kblocks;
     p.tiles_m = r.tiles_m;
     p.tiles_n = r.tiles_n;
-    p.splits = r.splits;
-    p.kb_split = r.kb_split;
-    p.items = (int64_t)r.tiles_m * r.tiles_n * r.splits;
+    p.tiles = r.tiles;
+    p.whole = r.whole;
+    p.pieces = r.pieces;
+    p.piece_kb = r.piece_kb;
     p.out = g.out;
     p.ld_out = g.ld_out;
     p.out_f32 = g.out_f32;
@@ -721,19 +838,24 @@ cudaError_t launch_ffn_product(const FfnProduct& g, cudaStream_t s)
     p.ld_u = g.ld_u;
     p.du = static_cast<bf16*>(g.du);
     p.ld_du = g.ld_du;
-    p.partial = g.partial;
-    if (r.splits == 1) {
-        if (g.epi == FFN_UP) return launch_shape<ffn::UP, false, false>(r.pair, ma, mb, p, s);
-        if (g.epi == FFN_DACT) return launch_shape<ffn::DACT, false, true>(r.pair, ma, mb, p, s);
-        return launch_layout<ffn::STORE>(r.pair, g.a_mn, g.b_mn, ma, mb, p, s);
-    }
-    ffn::Params q = p;
-    if (g.epi == FFN_UP) q.N = 2 * p.N;
-    cudaError_t e = launch_layout<ffn::PART>(r.pair, g.a_mn, g.b_mn, ma, mb, q, s);
-    if (e != cudaSuccess) return e;
-    if (g.epi == FFN_UP) return launch_join<ffn::UP>(p, s);
-    if (g.epi == FFN_DACT) return launch_join<ffn::DACT>(p, s);
-    return launch_join<ffn::STORE>(p, s);
+    p.slots = g.slots;
+    p.wide = on32(g.out, g.ld_out, g.out_f32 ? 4 : 2) && on32(g.u, g.ld_u, 2) && on32(g.du, g.ld_du, 2) &&
+             (g.epi == FFN_STORE || g.N % 16 == 0);
+    cudaError_t e;
+    if (g.epi == FFN_UP)
+        e = launch_shape<ffn::UP, false, false>(r.pair, ma, mb, p, after, s);
+    else if (g.epi == FFN_DACT)
+        e = launch_shape<ffn::DACT, false, true>(r.pair, ma, mb, p, after, s);
+    else if (g.a_mn)  // dW: both operands with M, N contiguous
+        e = launch_shape<ffn::STORE, true, true>(r.pair, ma, mb, p, after, s);
+    else if (g.b_mn)  // dx
+        e = launch_shape<ffn::STORE, false, true>(r.pair, ma, mb, p, after, s);
+    else  // y
+        e = launch_shape<ffn::STORE, false, false>(r.pair, ma, mb, p, after, s);
+    if (e != cudaSuccess || !r.pieces) return e;
+    if (g.epi == FFN_UP) return launch_join<ffn::UP>(r.pair, p, s);
+    if (g.epi == FFN_DACT) return launch_join<ffn::DACT>(r.pair, p, s);
+    return launch_join<ffn::STORE>(r.pair, p, s);
 }
 
 uint32_t ffn_device_error(bool clear)

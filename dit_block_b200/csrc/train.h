@@ -36,12 +36,13 @@ struct FfnProduct {
     int64_t ld_u;
     void* du;          // FFN_DACT
     int64_t ld_du;
-    float* partial;    // workspace of ffn_partial_bytes
+    float* slots;      // workspace of ffn_slot_bytes
 };
 
-// Bytes of f32 partial sums the product needs (0 where its inner dimension is not split).
-size_t ffn_partial_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K);
-cudaError_t launch_ffn_product(const FfnProduct& g, cudaStream_t s);
+// Bytes of f32 slots the product needs for the tiles that several workers share.
+size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K);
+// after: the kernel before on the stream is one of the same call, which may still be ending.
+cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s);
 // Error flags raised by these kernels' bounded waits; optionally cleared.  Synchronous.
 uint32_t ffn_device_error(bool clear);
 
