@@ -20,6 +20,9 @@ namespace adamw {
 constexpr int THREADS = 256;
 constexpr int BLOCK = SOL_ADAMW_BLOCK;
 constexpr int CHUNK = kAdamwChunk;
+#ifndef STEP8_CTAS
+#define STEP8_CTAS 4
+#endif
 constexpr int NORM_CTAS = 148 * 8;  // partial sums of the gradient norm
 static_assert((NORM_CTAS) * sizeof(double) <= SOL_ADAMW_NORM_WORKSPACE, "the norm's partial sums must fit its workspace");
 
@@ -59,13 +62,23 @@ __device__ __forceinline__ Live live_scalars(const Scalars& h)
     return l;
 }
 
-// One value: p, m, v in and out (fp32), g already widened.
+// sqrt with one MUFU operation, off by at most 2^-23 of itself; subnormal arguments count.
+__device__ __forceinline__ float sqrt_fast(float x)
+{
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One value: p, m, v in and out (fp32), g already widened.  The quotient is off by some
+// 2^-22 of the update, which is far below the rounding of p; its divisor stays below 2^65, as
+// __fdividef wants it.
 __device__ __forceinline__ void update(float& p, float& m, float& v, float g, float wd, const Scalars& h, const Live& l)
 {
     g *= l.factor;
     m = h.beta1 * m + h.one_minus1 * g;
     v = h.beta2 * v + h.one_minus2 * (g * g);
-    p -= l.lr * (wd * p + (m * l.inv_bc1) / (sqrtf(v * l.inv_bc2) + h.eps));
+    p -= l.lr * (wd * p + __fdividef(m * l.inv_bc1, sqrt_fast(v * l.inv_bc2) + h.eps));
 }
 
 __device__ __forceinline__ void load4(const float* p, float* f) { unpack<float>(ld_stream(p), f); }
@@ -138,122 +151,328 @@ __device__ __forceinline__ uint32_t mixed(uint32_t h)
     return h ^ (h >> 16);
 }
 
-__device__ __forceinline__ float decode_first(int q, float s)
+// Small whole numbers to fp32 and back without conversion instructions (which run at an
+// eighth of the rate of additions): 2^23 + q has q in its low mantissa bits.
+// Byte e of w, as 2^23 + byte; halfword e of w, as 2^23 + halfword (one byte permutation each).
+__device__ __forceinline__ float magic_byte(uint32_t w, int e)
 {
-    return (float)(q * abs(q)) * (1.f / 16129.f) * s;  // off by at most 3 * 2^-24
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u + e));
 }
-__device__ __forceinline__ float decode_second(uint32_t q, float s)
+__device__ __forceinline__ float magic_half(uint32_t w, int e)
 {
-    const float k2 = (float)(q * q) * (1.f / 65025.f);
-    return k2 * k2 * s;  // off by at most 6 * 2^-24
-}
-
-// Code of |x| (first) or x (second) in a block of scale s > 0, rounded up where the 16-bit
-// fraction r is below the place between the two neighbours.
-__device__ __forceinline__ int encode_first(float x, float s, float r)
-{
-    const float t = fabsf(x) / s * 16129.f;
-    float k = floorf(sqrtf(t));
-    if (r * fmaf(2.f, k, 1.f) < t - k * k) k += 1.f;
-    const int q = (int)fminf(k, 127.f);
-    return x < 0.f ? -q : q;
-}
-__device__ __forceinline__ uint32_t encode_second(float x, float s, float r)
-{
-    const float t = x / s * 4228250625.f;
-    float k = floorf(sqrtf(sqrtf(t)));
-    const float width = fmaf(fmaf(fmaf(4.f, k, 6.f), k, 4.f), k, 1.f), k2 = k * k;
-    if (r * width < t - k2 * k2) k += 1.f;
-    const uint32_t q = (uint32_t)fminf(k, 255.f);
-    return x > 0.f ? max(q, 1u) : 0u;
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, e ? 0x7532u : 0x7510u));
 }
 
-// Largest magnitude over a warp by the bits of |x| (NaN above infinity above all numbers),
-// as the block's scale: NaN where it is not finite.
-__device__ __forceinline__ float block_scale(uint32_t bits)
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A block's scale s as the decoders use it: k^power * unit, or, where s is so small that
+// unit would be subnormal, (k^power * step) * s.
+__device__ __forceinline__ float2 decode_unit(float s, float step)
 {
-    bits = __reduce_max_sync(0xffffffffu, bits);
+    return s < 1e-28f ? make_float2(step, s) : make_float2(step * s, 1.f);
+}
+// k * |k| and k^4 are formed with at most one rounding, the products add three more
+__device__ __forceinline__ float2 decode_first2(float2 z, float2 u)  // z: 2^23 + (code ^ 0x80)
+{
+    const float2 k = __fadd2_rn(z, both(-(8388608.f + 128.f)));
+    return __fmul2_rn(__fmul2_rn(make_float2(k.x * fabsf(k.x), k.y * fabsf(k.y)), both(u.x)), both(u.y));
+}
+__device__ __forceinline__ float2 decode_second2(float2 z, float2 u)  // z: 2^23 + code
+{
+    const float2 k = __fadd2_rn(z, both(-8388608.f)), k2 = __fmul2_rn(k, k);
+    return __fmul2_rn(__fmul2_rn(__fmul2_rn(k2, k2), both(u.x)), both(u.y));
+}
+constexpr float STEP1 = 1.f / 16129.f, STEP2 = (float)(1.0 / 4228250625.0);  // 127^-2, 255^-4
+
+// Eight codes (two words) of a block to values.
+__device__ __forceinline__ void decode_first8(uint2 q, float s, float2* m)
+{
+    const float2 u = decode_unit(s, STEP1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = (e < 2 ? q.x : q.y) ^ 0x80808080u;
+        m[e] = decode_first2(make_float2(magic_byte(w, 2 * (e & 1)), magic_byte(w, 2 * (e & 1) + 1)), u);
+    }
+}
+__device__ __forceinline__ void decode_second8(uint2 q, float s, float2* v)
+{
+    const float2 u = decode_unit(s, STEP2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = e < 2 ? q.x : q.y;
+        v[e] = decode_second2(make_float2(magic_byte(w, 2 * (e & 1)), magic_byte(w, 2 * (e & 1) + 1)), u);
+    }
+}
+
+__device__ __forceinline__ float root_ftz(float x)
+{
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// update() on two values: move = -lr / (1 - beta1^step), shrink = -lr * weight_decay.  ROOT_FTZ: the root of a subnormal v counts as zero.
+template <bool ROOT_FTZ>
+__device__ __forceinline__ void update2(float2& p, float2& m, float2& v, float2 g, float move, float shrink,
+                                        const Scalars& h, const Live& l)
+{
+    g = __fmul2_rn(g, both(l.factor));
+    m = __ffma2_rn(both(h.beta1), m, __fmul2_rn(both(h.one_minus1), g));
+    v = __ffma2_rn(both(h.beta2), v, __fmul2_rn(both(h.one_minus2), __fmul2_rn(g, g)));
+    const float2 x = __fmul2_rn(v, both(l.inv_bc2));
+    const float2 d = __fadd2_rn(
+        ROOT_FTZ ? make_float2(root_ftz(x.x), root_ftz(x.y)) : make_float2(sqrt_fast(x.x), sqrt_fast(x.y)), both(h.eps));
+    const float2 up = __ffma2_rn(__fmul2_rn(m, both(move)), make_float2(rcp_ftz(d.x), rcp_ftz(d.y)), p);
+    p = __ffma2_rn(both(shrink), p, up);
+}
+
+// Codes of two values.  t is a value in units of the table's first step.  Its root, made
+// smaller by 2^-20 of itself, minus a half, rounded to a whole number, is k: the root's floor, or one
+// less where the root is within 2^-20 above a whole number (so that the block's largest value
+// has k one below the table's end).  The value is stored as k + 1 where the 16-bit fraction h / 65536
+// is below (t - k^power) / ((k + 1)^power - k^power); at a k one too low that is always.
+// z holds k in its low byte (1.5 * 2^23 + k); the sign of s says whether to take k + 1.
+constexpr float MAGIC = 12582912.f, SHY = 1.f - 0x1p-20f;
+
+__device__ __forceinline__ void encode_first2(float2 x, float inv, uint32_t r0, uint32_t r1, float2& z, float2& s)
+{
+    const float2 minus_t = make_float2(fabsf(x.x) * -inv, fabsf(x.y) * -inv);
+    const float2 c = make_float2(root_ftz(-minus_t.x), root_ftz(-minus_t.y));
+    z = __fadd2_rn(__ffma2_rn(c, both(SHY), both(-0.5f)), both(MAGIC));
+    const float2 k = __fadd2_rn(z, both(-MAGIC));
+    const float2 h = __fadd2_rn(make_float2(magic_half(r0, 1), magic_half(r1, 1)), both(-8388608.f));
+    const float2 width = __ffma2_rn(both(2.f / 65536.f), k, both(1.f / 65536.f));
+    s = __ffma2_rn(h, width, __ffma2_rn(k, k, minus_t));
+}
+__device__ __forceinline__ void encode_second2(float2 x, float inv, uint32_t r0, uint32_t r1, float2& z, float2& s)
+{
+    float2 t = __fmul2_rn(x, both(inv));
+    t = make_float2(fmaxf(t.x, x.x > 0.f ? 1.f : 0.f), fmaxf(t.y, x.y > 0.f ? 1.f : 0.f));  // 1 at least
+    const float2 c = make_float2(root_ftz(root_ftz(t.x)), root_ftz(root_ftz(t.y)));
+    z = __fadd2_rn(__ffma2_rn(c, both(SHY), both(-0.5f)), both(MAGIC));
+    const float2 k = __fadd2_rn(z, both(-MAGIC)), k2 = __fmul2_rn(k, k);
+    const float2 h = __fadd2_rn(make_float2(magic_half(r0, 0), magic_half(r1, 0)), both(-8388608.f));
+    float2 width = __ffma2_rn(both(4.f / 65536.f), k, both(6.f / 65536.f));
+    width = __ffma2_rn(width, k, both(4.f / 65536.f));
+    width = __ffma2_rn(width, k, both(1.f / 65536.f));
+    s = __ffma2_rn(h, width, __ffma2_rn(k2, k2, make_float2(-t.x, -t.y)));
+}
+
+// The low bytes of four words; 0xff or 0 in each byte by the words' signs.
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b)
+{
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t prmt_sign(uint32_t a, uint32_t b)  // bytes 0 and 1: the signs of a and b
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, 0x00fb;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t sign_bytes(float2 a, float2 b)
+{
+    return __byte_perm(prmt_sign(__float_as_uint(a.x), __float_as_uint(a.y)),
+                       prmt_sign(__float_as_uint(b.x), __float_as_uint(b.y)), 0x5410);
+}
+// k or k + 1 of four values, a byte each (no byte can overflow); then negated where x < 0.
+__device__ __forceinline__ uint32_t four_codes(float2 z0, float2 z1, float2 s0, float2 s1)
+{
+    return low_bytes(z0, z1) + (sign_bytes(s0, s1) & 0x01010101u);
+}
+__device__ __forceinline__ uint32_t four_signed(uint32_t q, float2 x0, float2 x1)
+{
+    const uint32_t n = sign_bytes(x0, x1);
+    return (((q ^ n) & 0x7f7f7f7fu) + (n & 0x01010101u)) ^ (n & 0x80808080u);
+}
+
+// Largest magnitude of three, NaN if one is NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c)
+{
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// A block's scale from its lanes' largest magnitudes: by their bits (NaN above infinity above all
+// numbers), NaN where it is not finite.
+__device__ __forceinline__ float block_scale(float top)
+{
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
     return __uint_as_float(bits >= 0x7f800000u ? 0x7fffffffu : bits);
 }
 
-// A warp takes one block of 256 values, eight a lane; a CTA its 16 blocks in two rounds.
-template <typename G>
-__global__ void __launch_bounds__(THREADS) k_step8(const AdamwTable t, const __grid_constant__ Scalars h)
+// How a block's values are brought to units of the table's first step (`most` of them make up the
+// scale s): x * inv; for a small s, where most / s would overflow, x * 2^100 first.  A scale of
+// zero or NaN gives zero codes.
+struct Unit {
+    float pre, inv;
+};
+__device__ __forceinline__ Unit unit_of(float s, float most)
 {
+    Unit u;
+    u.pre = s < 1e-28f ? 1.2676506e30f : 1.f;
+    u.inv = s > 0.f ? most / (s * u.pre) : 0.f;
+    return u;
+}
+__device__ __forceinline__ void scale8(float2* x, float f)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(x[e], both(f));
+}
+
+// Everything that a lane does with its eight values of a block, all from registers.
+template <bool ROOT_FTZ>
+__device__ __forceinline__ void step_lane(float2* p, float2* m, float2* v, const float2* g, uint32_t at, int live, float wd,
+                                          const Scalars& h, const Live& l, uint2& q1, uint2& q2, float& n1, float& n2)
+{
+    float top1 = 0.f, top2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) update2<ROOT_FTZ>(p[e], m[e], v[e], g[e], -l.lr * l.inv_bc1, -l.lr * wd, h, l);
+    if (live < 8) {  // values past the tensor's end count for nothing
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (2 * e >= live) m[e].x = v[e].x = 0.f;
+            if (2 * e + 1 >= live) m[e].y = v[e].y = 0.f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        top1 = max_abs_nan(top1, m[e].x, m[e].y);
+        top2 = max_abs_nan(top2, v[e].x, v[e].y);
+    }
+    n1 = block_scale(top1);
+    n2 = block_scale(top2);
+    const Unit u1 = unit_of(n1, 16129.f), u2 = unit_of(n2, 4228250625.f);
+    if (u1.pre != 1.f) scale8(m, u1.pre);
+    if (u2.pre != 1.f) scale8(v, u2.pre);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float2 z[4], up[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t r0 = mixed(at + 4 * w + 2 * e), r1 = mixed(at + 4 * w + 2 * e + 1);
+            encode_first2(m[2 * w + e], u1.inv, r0, r1, z[e], up[e]);
+            encode_second2(v[2 * w + e], u2.inv, r0, r1, z[2 + e], up[2 + e]);
+        }
+        (w ? q1.y : q1.x) = four_signed(four_codes(z[0], z[1], up[0], up[1]), m[2 * w], m[2 * w + 1]);
+        (w ? q2.y : q2.x) = four_codes(z[2], z[3], up[2], up[3]);
+    }
+}
+
+// A lane's part of a block on its way through shared memory: every lane copies and reads its own
+// eight values only, so that no barrier is needed, and the next block's loads are in flight
+// while a block is worked on, without registers for them.
+template <typename G> struct alignas(16) LaneIn {
+    float p[8];
+    G g[8];
+    uint2 m, v;
+};
+
+__device__ __forceinline__ void copy16(void* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// A warp takes one block of 256 values at a time, eight a lane, two blocks in flight.
+template <typename G, bool ROOT_FTZ>
+__global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable t, const __grid_constant__ Scalars h)
+{
+    __shared__ LaneIn<G> in[2][THREADS];
     const AdamwChunk c = t.chunks[blockIdx.x];
     const AdamwTensor x = t.tensors[c.tensor];
     const Live l = live_scalars(h);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const G* grad = static_cast<const G*>(x.g);
-    int8_t* pm = static_cast<int8_t*>(x.m);
-    uint8_t* pv = static_cast<uint8_t*>(x.v);
+    uint8_t *pm = static_cast<uint8_t*>(x.m), *pv = static_cast<uint8_t*>(x.v);
     bf16* copy = static_cast<bf16*>(x.copy);
     const uint32_t key = mixed(mixed(mixed(x.ordinal * 0x9E3779B9u + l.step) ^ h.seed_hi) ^ h.seed_lo);
-    for (int b = warp; b < CHUNK / BLOCK; b += THREADS / 32) {
-        const int64_t start = (int64_t)c.index * CHUNK + b * BLOCK;
-        if (start >= x.n) break;
-        const int64_t i = start + 8 * lane, blk = start / BLOCK;
-        const int live = (int)min((int64_t)8, max((int64_t)0, x.n - i));
-        float p[8], g[8], m[8], v[8];
-        const float s1 = x.ms[blk], s2 = x.vs[blk];
-        if (live == 8) {
-            load4(x.p + i, p);
-            load4(x.p + i + 4, p + 4);
-            load4(grad + i, g);
-            load4(grad + i + 4, g + 4);
-            const uint2 q1 = __ldcs(reinterpret_cast<const uint2*>(pm + i));
-            const uint2 q2 = __ldcs(reinterpret_cast<const uint2*>(pv + i));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                m[e] = decode_first((int)(int8_t)((e < 4 ? q1.x : q1.y) >> (8 * (e & 3))), s1);
-                v[e] = decode_second(((e < 4 ? q2.x : q2.y) >> (8 * (e & 3))) & 255u, s2);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[e] = g[e] = m[e] = v[e] = 0.f;
-                if (e < live) {
-                    p[e] = x.p[i + e];
-                    g[e] = widen(grad[i + e]);
-                    m[e] = decode_first(pm[i + e], s1);
-                    v[e] = decode_second(pv[i + e], s2);
-                }
-            }
+    const int64_t base = (int64_t)c.index * CHUNK, end = min(x.n, base + CHUNK);
+    int64_t start = base + warp * BLOCK;
+    constexpr int STRIDE = THREADS / 32 * BLOCK;
+
+    auto fetch = [&](int64_t from, int stage) {  // whole blocks only
+        if (from + BLOCK <= end) {
+            LaneIn<G>& d = in[stage][threadIdx.x];
+            const int64_t i = from + 8 * lane;
+            copy16(d.p, x.p + i);
+            copy16(d.p + 4, x.p + i + 4);
+            copy16(d.g, grad + i);
+            if (sizeof(G) == 4) copy16(d.g + 4, grad + i + 4);
+            copy8(&d.m, pm + i);
+            copy8(&d.v, pv + i);
         }
-        uint32_t top1 = 0, top2 = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            update(p[e], m[e], v[e], g[e], x.wd, h, l);
-            if (e < live) {  // values past the tensor's end count for nothing
-                top1 = max(top1, __float_as_uint(m[e]) & 0x7fffffffu);
-                top2 = max(top2, __float_as_uint(v[e]) & 0x7fffffffu);
-            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float s1 = 0.f, s2 = 0.f;
+    if (start < end) {
+        s1 = x.ms[start / BLOCK];
+        s2 = x.vs[start / BLOCK];
+    }
+    fetch(start, 0);
+    for (int stage = 0; start < end; start += STRIDE, stage ^= 1) {
+        fetch(start + STRIDE, stage ^ 1);
+        const int64_t blk = start / BLOCK, i = start + 8 * lane;
+        float n1 = s1, n2 = s2;
+        if (start + STRIDE < end) {
+            s1 = x.ms[blk + THREADS / 32];
+            s2 = x.vs[blk + THREADS / 32];
         }
-        const float n1 = block_scale(top1), n2 = block_scale(top2);
-        uint2 q1 = make_uint2(0, 0), q2 = make_uint2(0, 0);
         const uint32_t at = mixed(key + (uint32_t)((uint64_t)start >> 32)) + (uint32_t)i;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t r = mixed(at + e);
-            const uint32_t a = n1 > 0.f ? (uint32_t)encode_first(m[e], n1, (float)(r >> 16) * (1.f / 65536.f)) & 255u : 0u;
-            const uint32_t w = n2 > 0.f ? encode_second(v[e], n2, (float)(r & 0xffffu) * (1.f / 65536.f)) : 0u;
-            (e < 4 ? q1.x : q1.y) |= a << (8 * (e & 3));
-            (e < 4 ? q2.x : q2.y) |= w << (8 * (e & 3));
-        }
-        if (live == 8) {
-            st_stream(x.p + i, pack<float>(p));
-            st_stream(x.p + i + 4, pack<float>(p + 4));
+        float2 p[4], g[4], m[4], v[4];
+        uint2 q1, q2;
+        if (start + BLOCK <= end) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            const LaneIn<G>& d = in[stage][threadIdx.x];
+            unpack2<float>(*reinterpret_cast<const uint4*>(d.p), p);
+            unpack2<float>(*reinterpret_cast<const uint4*>(d.p + 4), p + 2);
+            unpack2<G>(*reinterpret_cast<const uint4*>(d.g), g);
+            if (sizeof(G) == 4) unpack2<G>(*reinterpret_cast<const uint4*>(d.g + 4), g + 2);
+            decode_first8(d.m, n1, m);
+            decode_second8(d.v, n2, v);
+            step_lane<ROOT_FTZ>(p, m, v, g, at, 8, x.wd, h, l, q1, q2, n1, n2);
+            st_stream(x.p + i, pack2<float>(p));
+            st_stream(x.p + i + 4, pack2<float>(p + 2));
             *reinterpret_cast<uint2*>(pm + i) = q1;
             *reinterpret_cast<uint2*>(pv + i) = q2;
-            if (copy) st_stream(copy + i, pack<bf16>(p));
+            if (copy) st_stream(copy + i, pack2<bf16>(p));
         } else {
+            // the tensor's last block
+            const int live = (int)min((int64_t)8, max((int64_t)0, x.n - i));
+            float fp[8] = {}, fg[8] = {};
+            uint32_t w1[2] = {}, w2[2] = {};
+            for (int e = 0; e < live; ++e) {
+                fp[e] = x.p[i + e];
+                fg[e] = widen(grad[i + e]);
+                w1[e >> 2] |= (uint32_t)pm[i + e] << (8 * (e & 3));
+                w2[e >> 2] |= (uint32_t)pv[i + e] << (8 * (e & 3));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[e] = make_float2(fp[2 * e], fp[2 * e + 1]);
+                g[e] = make_float2(fg[2 * e], fg[2 * e + 1]);
+            }
+            decode_first8(make_uint2(w1[0], w1[1]), n1, m);
+            decode_second8(make_uint2(w2[0], w2[1]), n2, v);
+            step_lane<ROOT_FTZ>(p, m, v, g, at, live, x.wd, h, l, q1, q2, n1, n2);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (e < live) {
-                    x.p[i + e] = p[e];
-                    pm[i + e] = (int8_t)((e < 4 ? q1.x : q1.y) >> (8 * (e & 3)));
+                    const float pe = e & 1 ? p[e / 2].y : p[e / 2].x;
+                    x.p[i + e] = pe;
+                    pm[i + e] = (uint8_t)((e < 4 ? q1.x : q1.y) >> (8 * (e & 3)));
                     pv[i + e] = (uint8_t)((e < 4 ? q2.x : q2.y) >> (8 * (e & 3)));
-                    if (copy) copy[i + e] = __float2bfloat16_rn(p[e]);
+                    if (copy) copy[i + e] = __float2bfloat16_rn(pe);
                 }
         }
         if (lane == 0) {
@@ -266,18 +485,24 @@ __global__ void __launch_bounds__(THREADS) k_step8(const AdamwTable t, const __g
 // ---------------------------------------------------------------------------------
 // Global gradient norm.
 
-// Sum of squares of 16 values: scaled by a power of two near their largest magnitude,
-// squared and added in fp32, then brought back in fp64, so that neither 1e30 nor 1e-30 is
-// lost.  A non-finite value makes the sum infinite or NaN.
+// Sum of squares of 16 values.  Where the plain fp32 sum is neither close to overflow nor so
+// small that squares may have been lost (below 2^-126 each, nothing next to 2^-80), it is
+// taken; else the values are scaled by a power of two near their largest magnitude and the
+// sum is brought back in fp64, so that neither 1e30 nor 1e-30 is lost.  A non-finite value makes
+// the sum infinite or NaN.
 __device__ __forceinline__ double squares16(const float* g)
 {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s = fmaf(g[e], g[e], s);
+    if (s > 8.3e-25f && s < 1e38f) return (double)s;
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(g[e]) & 0x7fffffffu);
     if (top >= 0x7f800000u) return top == 0x7f800000u ? INFINITY : NAN;
     const uint32_t ex = min(max(top >> 23, 1u), 253u);  // biased exponent of the scale's inverse
     const float scale = __uint_as_float((254u - ex) << 23);
-    float s = 0.f;
+    s = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         const float y = g[e] * scale;
@@ -297,28 +522,34 @@ __device__ __forceinline__ double cta_sum(double v, double* buf)
     return s;
 }
 
+// The 16 values of a thread in a chunk, by 16-byte vectors, as 16 fp32 registers; zeros behind
+// the tensor's end.
+template <typename G> __device__ __forceinline__ void load16(const G* grad, int64_t base, int64_t n, float* g)
+{
+    constexpr int V = Vec<G>::N;
+#pragma unroll
+    for (int u = 0; u < 16 / V; ++u) {
+        const int64_t i = base + V * (u * THREADS + threadIdx.x);
+        if (i + V <= n) {
+            unpack<G>(ld_stream(grad + i), g + V * u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[V * u + e] = i + e < n ? widen(grad[i + e]) : 0.f;
+        }
+    }
+}
+
 // CTA b sums chunks b, b + gridDim.x, ...: the order depends on the plan alone.
 template <typename G>
-__global__ void __launch_bounds__(THREADS) k_norm_partial(const AdamwTable t, double* partial)
+__global__ void __launch_bounds__(THREADS, 8) k_norm_partial(const AdamwTable t, double* partial)
 {
     __shared__ double buf[THREADS / 32];
     double sum = 0.0;
     for (int64_t b = blockIdx.x; b < t.n_chunks; b += gridDim.x) {
         const AdamwChunk c = t.chunks[b];
         const AdamwTensor* x = t.tensors + c.tensor;
-        const G* grad = static_cast<const G*>(x->g);
-        const int64_t n = x->n, base = (int64_t)c.index * CHUNK;
         float g[16];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t i = base + 4 * (u * THREADS + threadIdx.x);
-            if (i + 4 <= n) {
-                load4(grad + i, g + 4 * u);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[4 * u + e] = i + e < n ? widen(grad[i + e]) : 0.f;
-            }
-        }
+        load16(static_cast<const G*>(x->g), (int64_t)c.index * CHUNK, x->n, g);
         sum += squares16(g);
     }
     sum = cta_sum(sum, buf);
@@ -339,37 +570,49 @@ __global__ void __launch_bounds__(THREADS) k_norm_final(float* out, const double
 }
 
 // Eight values a thread; the last thread's share may be smaller.
+template <typename T> __device__ __forceinline__ void put8(T* out, const float2* f, int live)
+{
+    if (live == 8) {
+#pragma unroll
+        for (int e = 0; e < 8; e += Vec<T>::N) st_stream(out + e, pack2<T>(f + e / 2));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < live) out[e] = (T)(e & 1 ? f[e / 2].y : f[e / 2].x);
+    }
+}
+__device__ __forceinline__ uint2 codes8(const uint8_t* q, int live)
+{
+    if (live == 8) return __ldcs(reinterpret_cast<const uint2*>(q));
+    uint32_t w[2] = {};
+    for (int e = 0; e < live; ++e) w[e >> 2] |= (uint32_t)q[e] << (8 * (e & 3));
+    return make_uint2(w[0], w[1]);
+}
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    k_decode(T* m_out, T* v_out, const int8_t* m, const uint8_t* v, const float* ms, const float* vs, int64_t n)
+    k_decode(T* m_out, T* v_out, const uint8_t* m, const uint8_t* v, const float* ms, const float* vs, int64_t n)
 {
     const int64_t i = 8 * ((int64_t)blockIdx.x * THREADS + threadIdx.x);
     if (i >= n) return;
-    const bool whole = i + 8 <= n;
-    float f[8];
+    const int live = (int)min((int64_t)8, n - i);
+    uint2 q1, q2;
+    float s1, s2;
     if (m_out) {
-        const float s = ms[i / BLOCK];
-        if (whole) {
-            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(m + i));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = decode_first((int)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3))), s);
-#pragma unroll
-            for (int e = 0; e < 8; e += Vec<T>::N) st_stream(m_out + i + e, pack<T>(f + e));
-        } else {
-            for (int64_t j = i; j < n; ++j) m_out[j] = (T)decode_first(m[j], s);
-        }
+        q1 = codes8(m + i, live);
+        s1 = __ldg(ms + i / BLOCK);
     }
     if (v_out) {
-        const float s = vs[i / BLOCK];
-        if (whole) {
-            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(v + i));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = decode_second(((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 255u, s);
-#pragma unroll
-            for (int e = 0; e < 8; e += Vec<T>::N) st_stream(v_out + i + e, pack<T>(f + e));
-        } else {
-            for (int64_t j = i; j < n; ++j) v_out[j] = (T)decode_second(v[j], s);
-        }
+        q2 = codes8(v + i, live);
+        s2 = __ldg(vs + i / BLOCK);
+    }
+    float2 f[4];
+    if (m_out) {
+        decode_first8(q1, s1, f);
+        put8(m_out + i, f, live);
+    }
+    if (v_out) {
+        decode_second8(q2, s2, f);
+        put8(v_out + i, f, live);
     }
 }
 
@@ -403,10 +646,12 @@ cudaError_t launch_adamw_step(const AdamwTable& t, sol_dtype grad_dt, int state_
         else
             adamw::k_step32<float><<<grid, adamw::THREADS, 0, s>>>(t, h);
     } else {
-        if (grad_dt == SOL_DTYPE_BF16)
-            adamw::k_step8<bf16><<<grid, adamw::THREADS, 0, s>>>(t, h);
-        else
-            adamw::k_step8<float><<<grid, adamw::THREADS, 0, s>>>(t, h);
+        // the root of a subnormal v (below 1e-19) is nothing next to an eps of 1e-12 or more
+        const bool ftz = a.eps >= 1e-12;
+        const auto kern = grad_dt == SOL_DTYPE_BF16
+                              ? (ftz ? adamw::k_step8<bf16, true> : adamw::k_step8<bf16, false>)
+                              : (ftz ? adamw::k_step8<float, true> : adamw::k_step8<float, false>);
+        kern<<<grid, adamw::THREADS, 0, s>>>(t, h);
     }
     return cudaGetLastError();
 }
@@ -434,10 +679,10 @@ cudaError_t launch_adamw_decode(void* m_out, void* v_out, sol_dtype out_dt, cons
     if (n == 0) return cudaSuccess;
     const unsigned grid = (unsigned)((n + 8 * adamw::THREADS - 1) / (8 * adamw::THREADS));
     if (out_dt == SOL_DTYPE_BF16)
-        adamw::k_decode<bf16><<<grid, adamw::THREADS, 0, s>>>((bf16*)m_out, (bf16*)v_out, (const int8_t*)m,
+        adamw::k_decode<bf16><<<grid, adamw::THREADS, 0, s>>>((bf16*)m_out, (bf16*)v_out, (const uint8_t*)m,
                                                               (const uint8_t*)v, ms, vs, n);
     else
-        adamw::k_decode<float><<<grid, adamw::THREADS, 0, s>>>((float*)m_out, (float*)v_out, (const int8_t*)m,
+        adamw::k_decode<float><<<grid, adamw::THREADS, 0, s>>>((float*)m_out, (float*)v_out, (const uint8_t*)m,
                                                                (const uint8_t*)v, ms, vs, n);
     return cudaGetLastError();
 }
