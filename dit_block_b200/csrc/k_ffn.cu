@@ -82,6 +82,7 @@ struct Params {
     int32_t tiles_m, tiles_n;
     int64_t whole, tiles;        // tiles [0, whole) are worked on whole, one after another by each worker
     int32_t pieces, piece_kb;    // tiles [whole, tiles): their K end to end in `pieces` of piece_kb blocks
+    int32_t stage_bytes;         // bytes that the copies of one CTA and stage bring
     int32_t a_blocks, b_blocks;  // 1: a copy brings both 64-row halves of the operand (see make_map)
     int32_t out_f32, accumulate;
     int32_t wide;                // rows of out, u and du (and their second halves) begin on 32-byte boundaries
@@ -238,7 +239,7 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
             if (remote)
                 bar = tc::mapa(bar, 0);
             else
-                mbar_arrive_expect_tx(bar, PAIR ? 2 * STAGE_BYTES : STAGE_BYTES);
+                mbar_arrive_expect_tx(bar, PAIR ? 2 * p.stage_bytes : p.stage_bytes);
             load_operand<A_MN>(dst, tmA, p.a_blocks, ma, ma + BOX, kb * BK, bar, remote);
             load_operand<B_MN>(dst + OP_BYTES, tmB, p.b_blocks, n0, n1, kb * BK, bar, remote);
             last[s] = (int32_t)phase;
@@ -671,19 +672,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 
 // Tensor map of an operand in the 128-byte swizzle; what lies outside the tensor reads as zero.  Sets
 // *both where one copy brings both 64-row halves of a 128-row tile:
-//   K contiguous: boxes of 64 K x 128 rows (not where the halves are apart: `halves`);
+//   K contiguous: boxes of 64 K x `rows` rows, 128 or, where the only tile has fewer, as many as it has (rows
+//   of the shared-memory tile that nothing is copied to give accumulator rows that nothing reads);
+//   64 where the halves are apart;
 //   M (N) contiguous: the 64-wide column blocks as a third dimension, boxes of 64 x 64 x 2, where the width
 //   is a multiple of 64, so that no block reaches into the next row.
-bool make_map(CUtensorMap* m, const Mat& t, bool mn, bool halves, int32_t* both)
+bool make_map(CUtensorMap* m, const Mat& t, bool mn, int32_t rows, int32_t* both)
 {
     auto fn = encode_fn();
     if (!fn) return false;
     const bool blocks = mn && t.cols % ffn::BOX == 0;
-    *both = mn ? blocks : !halves;
+    *both = mn ? blocks : rows != ffn::BOX;
     const cuuint64_t dims[3] = {(cuuint64_t)(blocks ? ffn::BOX : t.cols), (cuuint64_t)t.rows,
                                 (cuuint64_t)(t.cols / ffn::BOX)};
     const cuuint64_t strides[2] = {(cuuint64_t)t.ld * 2, ffn::BOX * 2};
-    const cuuint32_t box[3] = {ffn::BOX, (cuuint32_t)(mn || halves ? ffn::BOX : 2 * ffn::BOX), 2};
+    const cuuint32_t box[3] = {ffn::BOX, (cuuint32_t)(mn ? ffn::BOX : rows), 2};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, blocks ? 3 : 2, const_cast<void*>(t.p), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -816,8 +819,11 @@ cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
     CUtensorMap ma, mb;
     const Plan r = plan(g.epi, g.M, g.N, g.K);
     ffn::Params p{};
-    if (!make_map(&ma, g.a, g.a_mn, false, &p.a_blocks) ||
-        !make_map(&mb, g.b, g.b_mn, g.epi == FFN_UP && !r.pair, &p.b_blocks)) {
+    int32_t a_rows = !r.pair && !g.a_mn && r.tiles_m == 1 ? (int32_t)((g.M + 7) / 8 * 8) : ffn::BM;
+    if (a_rows == ffn::BOX) a_rows += 8;  // 64 means two boxes
+    p.stage_bytes = ffn::OP_BYTES + a_rows * ffn::BK * 2;
+    if (!make_map(&ma, g.a, g.a_mn, a_rows, &p.a_blocks) ||
+        !make_map(&mb, g.b, g.b_mn, g.epi == FFN_UP && !r.pair ? ffn::BOX : ffn::BM, &p.b_blocks)) {
         record_error("tensor map encoding failed (cuTensorMapEncodeTiled unavailable or refused the layout)");
         return cudaErrorInvalidValue;
     }

@@ -195,6 +195,10 @@ sol_status sol_ffn(void* y, int64_t ld_y, void* u, int64_t ld_u, const void* x, 
     TRY(check_apart(written, 3, read, 3));
     const cudaStream_t s = (cudaStream_t)stream;
     void* act = (char*)workspace + lay.act;
+    if (sol::ffn_small_fits(T, d, inner)) {
+        const sol::FfnSmall f{(int32_t)T, (int32_t)d, (int32_t)inner, x, w_up, w_down, ld_x, ld_wu, ld_wd, y, u, act, ld_y, ld_u};
+        return cuda_status(sol::launch_ffn_small(f, s), "sol_ffn launch");
+    }
     sol::FfnProduct g = product(sol::FFN_UP, T, inner, d, {x, T, d, ld_x}, false, {w_up, 2 * inner, d, ld_wu}, false,
                                 act, inner, workspace, lay);
     g.u = u;

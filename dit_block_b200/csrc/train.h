@@ -43,6 +43,27 @@ struct FfnProduct {
 size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K);
 // after: the kernel before on the stream is one of the same call, which may still be ending.
 cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s);
+
+// The whole forward pass for a few tokens (k_ffn_small.cu).  Measured at d x inner, us, against
+// k_ffn.cu:   1 token   5120 x 13824  69.8 : 83.5    1000 x 2504   6.0 : 19.0
+//            16 tokens  5120 x 13824  93 : 82.5      3000 x 8000  47 : 37     1000 x 2504   8.5 : 20
+//            32 tokens  5120 x 13824 142 : 85.6      1024 x 4096  15 : 20      256 x 512    5.7 : 9.2
+// k_ffn.cu takes some 14 us beside the weights' bytes at 6.2 TB/s; this one 3 us, with 6 TB/s for
+// up to 8 tokens, and about 3.3 and 2.2 TB/s for up to 16 and 32, where the tokens' values cost as
+// many loads as the weights: the two meet at 78 and 38 MB of weights.
+inline bool ffn_small_fits(int64_t T, int64_t d, int64_t inner)
+{
+    return T <= 8 || (T <= 16 && d * inner <= 13000000) || (T <= 32 && d * inner <= 6300000);
+}
+struct FfnSmall {
+    int32_t T, d, inner;
+    const void *x, *w_up, *w_down;
+    int64_t ld_x, ld_wu, ld_wd;
+    void *y, *u, *act;  // u may be NULL; act [T, inner] is workspace
+    int64_t ld_y, ld_u;
+};
+cudaError_t launch_ffn_small(const FfnSmall& f, cudaStream_t s);
+
 // Error flags raised by these kernels' bounded waits; optionally cleared.  Synchronous.
 uint32_t ffn_device_error(bool clear);
 

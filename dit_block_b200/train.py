@@ -63,41 +63,39 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _device(*tensors) -> torch.device:
-    """The one CUDA device that all given tensors lie on."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libsol takes CUDA tensors")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: all of a call's tensors lie on one device")
-        dev = t.device
-    return dev
+def _on(index: int):
+    """Makes a device the current one for a call."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _on(dev: torch.device):
-    """Makes `dev` the current device for a call."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _device(t) -> int:
+    """The index of the CUDA device that a call's first tensor lies on; the others must lie there too."""
+    if not t.is_cuda:
+        raise ValueError("libsol takes CUDA tensors")
+    return t.get_device()
 
 
-def _matrix(name: str, t, rows: int, cols: int, *dtypes):
-    if t is None:
-        return
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+def _matrix(name: str, t, rows: int, cols: int, dtype, device: int):
+    """(address, row stride) of a [rows, cols] argument; a single row may have any stride."""
+    if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}, as the call's other tensors")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), s0 if rows > 1 else cols
 
 
-def _ld(t) -> int:
-    """Row stride; a single row may have any."""
-    if t is None:
-        return 0
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("tensors must have unit column stride")
-    return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
+def _space(workspace, device: int):
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace must be a CUDA tensor on device {device}, as the call's other tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+_NONE = (None, 0)
 
 
 # ---------------------------------------------------------------- gated feed-forward block
@@ -121,15 +119,12 @@ def ffn(y, x, w_up, w_down, *, u=None, workspace, stream=None):
     bf = torch.bfloat16
     n, d = x.shape
     inner = w_down.shape[1]
-    for name, t, r, c in (("x", x, n, d), ("y", y, n, d), ("w_up", w_up, 2 * inner, d), ("w_down", w_down, d, inner),
-                          ("u", u, n, 2 * inner)):
-        _matrix(name, t, r, c, bf)
-    dev = _device(x, y, w_up, w_down, u, workspace)
+    dev = _device(x)
+    args = (*_matrix("y", y, n, d, bf, dev), *(_NONE if u is None else _matrix("u", u, n, 2 * inner, bf, dev)),
+            *_matrix("x", x, n, d, bf, dev), *_matrix("w_up", w_up, 2 * inner, d, bf, dev),
+            *_matrix("w_down", w_down, d, inner, bf, dev), *_space(workspace, dev), n, d, inner, sol.BF16)
     with _on(dev):
-        sol._check(lib().sol_ffn(sol._ptr(y), _ld(y), sol._ptr(u), _ld(u), sol._ptr(x), _ld(x), sol._ptr(w_up), _ld(w_up),
-                                 sol._ptr(w_down), _ld(w_down), sol._ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), n, d, inner, sol.BF16,
-                                 sol._stream(stream)), "sol_ffn")
+        sol._check((_lib or lib()).sol_ffn(*args, sol._stream(stream)), "sol_ffn")
     return y
 
 
@@ -138,34 +133,35 @@ def ffn_backward(dy, x, u, w_up, w_down, *, dx=None, dw_up=None, dw_down=None, a
     """Gradients of ffn from dy and the u that it kept (sol_ffn_backward): dx [n, d] bf16, dw_up and
     dw_down in bf16 or f32 (both of one type), each only where given; accumulate adds to the
     weight gradients' contents."""
-    bf, f32 = torch.bfloat16, torch.float32
+    bf = torch.bfloat16
     n, d = x.shape
     inner = w_down.shape[1]
-    for name, t, r, c in (("dy", dy, n, d), ("x", x, n, d), ("u", u, n, 2 * inner), ("w_up", w_up, 2 * inner, d),
-                          ("w_down", w_down, d, inner), ("dx", dx, n, d)):
-        _matrix(name, t, r, c, bf)
-    _matrix("dw_up", dw_up, 2 * inner, d, bf, f32)
-    _matrix("dw_down", dw_down, d, inner, bf, f32)
-    types = {t.dtype for t in (dw_up, dw_down) if t is not None}
-    if len(types) > 1:
-        raise TypeError("dw_up and dw_down must have one type")
-    grad_dt = sol.F32 if types == {f32} else sol.BF16
-    dev = _device(dy, x, u, w_up, w_down, dx, dw_up, dw_down, workspace)
+    grad = bf if dw_up is None and dw_down is None else (dw_down if dw_up is None else dw_up).dtype
+    if grad is not bf and grad is not torch.float32:
+        raise TypeError(f"dw_up and dw_down must be torch.bfloat16 or torch.float32, got {grad}")
+    dev = _device(x)
+    args = (*(_NONE if dx is None else _matrix("dx", dx, n, d, bf, dev)),
+            *(_NONE if dw_up is None else _matrix("dw_up", dw_up, 2 * inner, d, grad, dev)),
+            *(_NONE if dw_down is None else _matrix("dw_down", dw_down, d, inner, grad, dev)),
+            sol.BF16 if grad is bf else sol.F32, 1 if accumulate else 0, *_matrix("dy", dy, n, d, bf, dev),
+            *_matrix("x", x, n, d, bf, dev), *_matrix("u", u, n, 2 * inner, bf, dev),
+            *_matrix("w_up", w_up, 2 * inner, d, bf, dev), *_matrix("w_down", w_down, d, inner, bf, dev),
+            *_space(workspace, dev), n, d, inner, sol.BF16)
     with _on(dev):
-        sol._check(lib().sol_ffn_backward(
-            sol._ptr(dx), _ld(dx), sol._ptr(dw_up), _ld(dw_up), sol._ptr(dw_down), _ld(dw_down), grad_dt,
-            int(bool(accumulate)), sol._ptr(dy), _ld(dy), sol._ptr(x), _ld(x), sol._ptr(u), _ld(u), sol._ptr(w_up),
-            _ld(w_up), sol._ptr(w_down), _ld(w_down), sol._ptr(workspace), workspace.numel() * workspace.element_size(),
-            n, d, inner, sol.BF16, sol._stream(stream)), "sol_ffn_backward")
+        sol._check((_lib or lib()).sol_ffn_backward(*args, sol._stream(stream)), "sol_ffn_backward")
 
 
 # ---------------------------------------------------------------------------------- AdamW
 
-def _flat(name, t, n, dtype):
-    if t.dtype != dtype:
+def _flat(name, t, n, dtype, device: int):
+    """Address of a contiguous argument of n values."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} values")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}, as the call's other tensors")
+    return t.data_ptr()
 
 
 class AdamW:
@@ -189,25 +185,21 @@ class AdamW:
         if grad_type not in (torch.float32, torch.bfloat16):
             raise TypeError(f"gradients must be float32 or bfloat16, got {grad_type}")
         rows = (AdamwTensor * max(n, 1))()
-        kept = []
+        dev = _device(params[0]) if n else torch.cuda.current_device()
+        first, second = (torch.int8, torch.uint8) if bits == 8 else (torch.float32, torch.float32)
         for i in range(n):
             k = params[i].numel()
-            _flat("param", params[i], k, torch.float32)
-            _flat("grad", grads[i], k, grad_type)
-            _flat("m", m[i], k, torch.int8 if bits == 8 else torch.float32)
-            _flat("v", v[i], k, torch.uint8 if bits == 8 else torch.float32)
-            if copies[i] is not None:
-                _flat("copy", copies[i], k, torch.bfloat16)
-            for s in scales[i]:
-                if bits == 8:
-                    _flat("scale", s, -(-k // BLOCK), torch.float32)
-            one = (params[i], copies[i], grads[i], m[i], v[i], *scales[i])
-            kept.append(one)
-            rows[i] = AdamwTensor(*(sol._ptr(t) for t in one), k, decay[i])
-        self._kept = kept
-        self.device = _device(*(t for one in kept for t in one)) or torch.device("cuda", torch.cuda.current_device())
+            blocks = -(-k // BLOCK)
+            rows[i] = AdamwTensor(
+                _flat("param", params[i], k, torch.float32, dev),
+                None if copies[i] is None else _flat("copy", copies[i], k, torch.bfloat16, dev),
+                _flat("grad", grads[i], k, grad_type, dev), _flat("m", m[i], k, first, dev), _flat("v", v[i], k, second, dev),
+                *(None if s is None else _flat("scale", s, blocks, torch.float32, dev) for s in scales[i]), k, decay[i])
+        self._kept = (list(params), list(grads), list(m), list(v), copies, scales)
+        self.device = torch.device("cuda", dev)
+        self._index = dev
         h = _P()
-        with _on(self.device):
+        with _on(dev):
             sol._check(lib().sol_adamw_plan_create(ctypes.byref(h), rows, n,
                                                    sol.BF16 if grad_type == torch.bfloat16 else sol.F32, bits),
                        "sol_adamw_plan_create")
@@ -217,16 +209,13 @@ class AdamW:
              grad_factor=None, stream=None):
         """One step (sol_adamw_step).  lr_device (f32) and step_device (int64) are device scalars read in place
         of lr and step when the step runs; grad_factor (f32) multiplies the gradients."""
-        for name, t, dtype in (("lr_device", lr_device, torch.float32), ("step_device", step_device, torch.int64),
-                               ("grad_factor", grad_factor, torch.float32)):
-            if t is not None:
-                _flat(name, t, 1, dtype)
-                if t.device != self.device:
-                    raise ValueError(f"{name} must lie on {self.device}")
-        h = AdamwScalars(float(lr), float(betas[0]), float(betas[1]), float(eps), int(step), int(seed) & (2 ** 64 - 1),
-                         sol._ptr(lr_device), sol._ptr(step_device), sol._ptr(grad_factor))
-        with _on(self.device):
-            sol._check(lib().sol_adamw_step(self._handle, ctypes.byref(h), sol._stream(stream)), "sol_adamw_step")
+        dev = self._index
+        h = AdamwScalars(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFFFFFFFFFF,
+                         None if lr_device is None else _flat("lr_device", lr_device, 1, torch.float32, dev),
+                         None if step_device is None else _flat("step_device", step_device, 1, torch.int64, dev),
+                         None if grad_factor is None else _flat("grad_factor", grad_factor, 1, torch.float32, dev))
+        with _on(dev):
+            sol._check(_lib.sol_adamw_step(self._handle, ctypes.byref(h), sol._stream(stream)), "sol_adamw_step")
 
     def norm_workspace(self) -> torch.Tensor:
         """A workspace for grad_norm (one for each of the calls that may overlap)."""
@@ -234,20 +223,17 @@ class AdamW:
 
     def grad_norm(self, out, max_norm, *, workspace, stream=None):
         """out[0] = norm of all gradients, out[1] = min(1, max_norm / (out[0] + 1e-6))  (sol_adamw_grad_norm)."""
-        _flat("out", out, 2, torch.float32)
-        if _device(out, workspace) != self.device:
-            raise ValueError(f"out and workspace must lie on {self.device}")
-        with _on(self.device):
-            sol._check(lib().sol_adamw_grad_norm(sol._ptr(out), self._handle, float(max_norm), sol._ptr(workspace),
-                                                 workspace.numel() * workspace.element_size(), sol._stream(stream)),
-                       "sol_adamw_grad_norm")
+        dev = self._index
+        args = (_flat("out", out, 2, torch.float32, dev), self._handle, max_norm, *_space(workspace, dev))
+        with _on(dev):
+            sol._check(_lib.sol_adamw_grad_norm(*args, sol._stream(stream)), "sol_adamw_grad_norm")
         return out
 
     def close(self):
         """Frees the plan: its steps have ended, and no captured graph that uses it is replayed any more."""
         if self._handle:
             h, self._handle = self._handle, None
-            with _on(self.device):
+            with _on(self._index):
                 sol._check(lib().sol_adamw_plan_destroy(h), "sol_adamw_plan_destroy")
             self._kept = None
 
@@ -267,17 +253,20 @@ class AdamW:
 def adamw_state_decode(m_out, v_out, m, v, m_scale, v_scale, *, stream=None):
     """The values that 8-bit moments stand for (sol_adamw_state_decode); m_out and v_out (either may be
     None) share one type, f32 or bf16."""
-    outs = [t for t in (m_out, v_out) if t is not None]
-    if not outs:
+    out = v_out if m_out is None else m_out
+    if out is None:
         return
-    n = outs[0].numel()
-    for name, out, q, s, dtype in (("m", m_out, m, m_scale, torch.int8), ("v", v_out, v, v_scale, torch.uint8)):
-        if out is not None:
-            _flat(name + "_out", out, n, outs[0].dtype)
-            _flat(name, q, n, dtype)
-            _flat(name + "_scale", s, -(-n // BLOCK), torch.float32)
-    dev = _device(*outs, *(t for o, q, s in ((m_out, m, m_scale), (v_out, v, v_scale)) if o is not None for t in (q, s)))
+    n, dtype, dev = out.numel(), out.dtype, _device(out)
+    blocks = -(-n // BLOCK)
+
+    def part(name, o, q, s, codes):
+        if o is None:
+            return None, None, None
+        return (_flat(name + "_out", o, n, dtype, dev), _flat(name, q, n, codes, dev),
+                _flat(name + "_scale", s, blocks, torch.float32, dev))
+
+    mo, mq, ms = part("m", m_out, m, m_scale, torch.int8)
+    vo, vq, vs = part("v", v_out, v, v_scale, torch.uint8)
     with _on(dev):
-        sol._check(lib().sol_adamw_state_decode(sol._ptr(m_out), sol._ptr(v_out), sol._dtype(outs[0]), sol._ptr(m),
-                                                sol._ptr(v), sol._ptr(m_scale), sol._ptr(v_scale), n, sol._stream(stream)),
+        sol._check((_lib or lib()).sol_adamw_state_decode(mo, vo, sol._dtype(out), mq, vq, ms, vs, n, sol._stream(stream)),
                    "sol_adamw_state_decode")

@@ -21,7 +21,8 @@ BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
 HALF, ACC, FN = 2.0 ** -8, 2.0 ** -23, 2.0 ** -20
 
 SIZES = [  # n_tokens, d, inner
-    (1, 8, 8), (1, 256, 512), (2, 64, 128), (7, 72, 1032), (31, 264, 136), (64, 128, 64), (128, 256, 512),
+    (1, 8, 8), (1, 256, 512), (2, 64, 128), (7, 72, 1032), (31, 264, 136), (8, 136, 72), (9, 520, 264), (16, 64, 8200), (16, 1000, 336), (17, 72, 80), (57, 64, 72),
+    (63, 128, 64), (64, 128, 64), (65, 72, 64), (120, 64, 128), (128, 256, 512),
     (129, 64, 200), (257, 1000, 328), (1000, 200, 2504), (4099, 64, 64), (300, 2560, 1024),
 ]
 

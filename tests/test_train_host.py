@@ -209,18 +209,27 @@ def test_binding_refuses_cpu_tensors_shapes_and_types():
     ws = torch.zeros(1024, dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA"):
         train.ffn(torch.zeros_like(x), x, wu, wd, workspace=ws)
-    with pytest.raises(ValueError, match="w_up must be"):
-        train.ffn(torch.zeros_like(x), x, wu[:128], wd, workspace=ws)
-    with pytest.raises(TypeError, match="x must be"):
-        train.ffn(torch.zeros_like(x), x.float(), wu, wd, workspace=ws)
-    with pytest.raises(TypeError, match="one type"):
-        train.ffn_backward(x, x, torch.zeros(4, 256, dtype=bf), wu, wd, dw_up=wu.float(), dw_down=wd.clone(), workspace=ws)
+    with pytest.raises(TypeError, match="dw_up and dw_down must be"):
+        train.ffn_backward(x, x, torch.zeros(4, 256, dtype=bf), wu, wd, dw_up=wu.double(), workspace=ws)
+    check = train._matrix
+    with pytest.raises(ValueError, match=r"w_up must be \[256, 64\]"):
+        check("w_up", wu[:128], 256, 64, bf, -1)
+    with pytest.raises(TypeError, match="x must be torch.bfloat16"):
+        check("x", x.float(), 4, 64, bf, -1)
+    with pytest.raises(ValueError, match="unit column stride"):
+        check("x", x.repeat(1, 2)[:, ::2], 4, 64, bf, -1)
+    with pytest.raises(ValueError, match="on device 0"):
+        check("x", x, 4, 64, bf, 0)
+    assert check("x", x, 4, 64, bf, -1) == (x.data_ptr(), 64)
+    assert check("x", x[:1], 1, 64, bf, -1)[1] == 64
     p = [torch.zeros(8)]
     with pytest.raises(ValueError, match="CUDA"):
         train.AdamW(p, p, p, p)
-    with pytest.raises(TypeError, match="m must be"):
-        train.AdamW(p, p, p, p, m_scales=[torch.zeros(1)], v_scales=[torch.zeros(1)])
     with pytest.raises(ValueError, match="one entry"):
         train.AdamW(p, p, p, p, weight_decay=[0.0, 0.0])
+    with pytest.raises(TypeError, match="gradients must be"):
+        train.AdamW(p, [p[0].double()], p, p)
     with pytest.raises(ValueError, match="contiguous"):
-        train.AdamW(p, [torch.zeros(16)[::2]], p, p)
+        train._flat("grad", torch.zeros(16)[::2], 8, torch.float32, -1)
+    with pytest.raises(TypeError, match="m must be"):
+        train._flat("m", torch.zeros(8), 8, torch.int8, -1)
