@@ -50,8 +50,12 @@ constexpr int BOX = 64;                    // a box is BOX x BOX
 constexpr int BOX_BYTES = BOX * BOX * 2;   // 8 KiB
 constexpr int OP_BYTES = 2 * BOX_BYTES;    // one operand of a stage
 constexpr int STAGE_BYTES = 2 * OP_BYTES;  // 32 KiB
-constexpr int STAGES = 7;
-constexpr int GROUP_M = 16;                // m-blocks per raster group (L2 reuse)
+constexpr int STAGES = 5;                  // as fast as 6 and 7, and leaves room for the epilogue
+constexpr int EPI_BYTES = 49152;           // staging of the epilogue warps
+// m-blocks per raster group: 74 pairs then work on 8 x 9 tiles at a time, which read the fewest
+// distinct rows of A and B.  DRAM reads of dx and dW_up at 31,248 tokens 13.4 GB each, 14.4 (and up
+// to 25) with 16, 19 with 4; the whole backward pass 21.6 against 22.5 ms at the power cap.
+constexpr int GROUP_M = 8;
 constexpr int EPI_WARP0 = 2;
 constexpr uint32_t kWaitLimit = 4096;      // polls of <= ~1 ms each
 constexpr uint32_t kPollLimit = 1u << 26;  // polls without a suspend hint
@@ -69,11 +73,12 @@ __host__ __device__ constexpr int block_threads(int mode) { return 64 + 32 * epi
 
 struct Bars {
     uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drain;
+    uint64_t u_full[8];         // DACT: a warp's pieces of u have landed
     int32_t peer_last[STAGES];  // leader: phase of the peer's last copy per stage (-1: none)
     uint32_t tmem_base;
     volatile int32_t abort;
 };
-constexpr size_t kSmemBytes = 1024 + (size_t)STAGES * STAGE_BYTES + sizeof(Bars);
+constexpr size_t kSmemBytes = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + sizeof(Bars);
 
 __device__ uint32_t g_error;
 
@@ -104,6 +109,12 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr)
     return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(BOX_BYTES >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
            ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
+
+// Tensor maps of one launch: the operands, and what the epilogue copies through shared memory
+// (STORE: out; UP and DACT: act, the halves of u, the halves of du; boxes as in out_map).
+struct Maps {
+    CUtensorMap a, b, out, u_a, u_b, du_a, du_b;
+};
 
 // A piece of work: K blocks [kb0, kb1) of a tile; slot >= 0 where they are not all of its K.
 struct Piece {
@@ -445,51 +456,78 @@ __device__ __forceinline__ void finish16(const Params& p, int64_t row, int32_t c
 // Columns of [col, col + 16) inside a width of N (a multiple of 8).
 __device__ __forceinline__ int inside(int32_t col, int32_t N) { return min(max(N - col, 0), 16); }
 
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// Staging of an epilogue warp: boxes of 32 rows, a row a lane, of 32 columns (64 bytes, 64-byte
+// swizzle) or 64 columns (128 bytes, 128-byte swizzle).  Address of 16-byte vector c of a row:
+// the eight lanes of a quarter-warp hit eight different bank groups.
+__device__ __forceinline__ uint32_t cell64(uint32_t box, int row, int c) { return box + row * 64 + ((c ^ (row >> 1)) & 3) * 16; }
+__device__ __forceinline__ uint32_t cell128(uint32_t box, int row, int c) { return box + row * 128 + ((c ^ row) & 7) * 16; }
+constexpr int BOX32 = 32 * 64, BOX64 = 32 * 128;
+
 // Epilogue: thread (warp w, lane l) owns accumulator row 32 * (w % 4) + l of this CTA and,
-// with eight warps, half of its columns.
-template <int MODE, bool PAIR> __device__ void run_epilogue(const Params& p, Bars* b, const Where& w)
+// with eight warps, half of its columns.  bf16 outputs go through shared memory and leave as
+// tensor copies: whole rows of 64 or 128 bytes, clipped to the tensor, and no thread waits for
+// them.  (Straight from registers a warp's store touched 32 rows; at d 1000, width 2504, 4,099
+// tokens, d_act took 83 us.)  DACT brings u the same way, the first piece of a tile while its
+// product still runs.
+template <int MODE, bool PAIR>
+__device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging, Bars* b, const Where& w)
 {
     constexpr int EW = epi_warps(MODE), H = EW / 4, TN = tile_n<PAIR>(), TM = tile_m<PAIR>();
     constexpr int WIDTH = MODE == UP ? TN / 2 : TN;  // UP: a in columns [0, WIDTH), b behind them
-    constexpr int CH = WIDTH / 32;
+    constexpr int CH = WIDTH / 32 / H;               // steps of 32 columns of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, part = (warp - EPI_WARP0) / 4;
+    const uint32_t box = staging + (warp - EPI_WARP0) * (EPI_BYTES / EW);
+    const uint32_t u_bar = smem_u32(&b->u_full[(warp - EPI_WARP0) & 7]);
+    uint32_t u_phase = 0;
+    bool u_pending = false, ok = true;
     int64_t n = 0;
     Walk walk = walk_begin(w.worker);
     Piece it;
-    for (; walk_next(walk, p, w.n_workers, it); ++n) {
+    for (; ok && walk_next(walk, p, w.n_workers, it); ++n) {
         const int ab = (int)(n & 1);
+        const int32_t row0 = it.m_blk * TM + (int32_t)w.rank * BM + quarter * 32;  // of this warp
+        const int32_t col0 = it.n_blk * WIDTH + part * CH * 32;
+        const bool whole = it.slot < 0;
+        auto fetch_u = [&](int32_t col) {  // lane 0, once the boxes are free
+            if (lane == 0) {
+                tc::bulk_wait_read<0>();
+                mbar_arrive_expect_tx(u_bar, 2 * BOX32);
+                tc::tma_load_2d(box, &maps.u_a, col, row0, u_bar);
+                tc::tma_load_2d(box + BOX32, &maps.u_b, col, row0, u_bar);
+            }
+            u_pending = true;
+        };
+        if (MODE == DACT && whole && row0 < p.M && col0 < p.N) fetch_u(col0);
         const bool got = wait_or_abort<PAIR>(smem_u32(&b->acc_full[ab]), (uint32_t)((n >> 1) & 1), b);
         if (!__all_sync(0xffffffffu, got)) {
             raise_abort(b, 32u);
             break;
         }
         tc::fence_after_sync();
-        const int tile_row = (int)w.rank * BM + quarter * 32 + lane;
-        const int64_t row = (int64_t)it.m_blk * TM + tile_row;
-        const bool live = row < p.M;
-        const uint32_t t = b->tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ab * TN);
+        const uint32_t t = b->tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ab * TN) + part * CH * 32;
         float v[32], g[MODE == UP ? 32 : 1];
 #pragma unroll 1
-        for (int c = part * (CH / H); c < (part + 1) * (CH / H); ++c) {
-            const int32_t col = it.n_blk * WIDTH + 32 * c;
-            const int n0 = inside(col, p.N), n1 = inside(col + 16, p.N);
-            uint4 ua[4], ub[4];
-            if (MODE == DACT && live && it.slot < 0) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = h ? n1 : n0;
-                    if (!k) break;
-                    get16(p.u + row * p.ld_u + col + 16 * h, ua[2 * h], ua[2 * h + 1], k, p.wide);
-                    get16(p.u + row * p.ld_u + p.N + col + 16 * h, ub[2 * h], ub[2 * h + 1], k, p.wide);
-                }
-            }
+        for (int c = 0; c < CH && ok; ++c) {
+            const int32_t col = col0 + 32 * c;
             tc::ld32(t + 32 * c, v);
             if constexpr (MODE == UP) tc::ld32(t + WIDTH + 32 * c, g);
-            if (!live) continue;
-            if (it.slot >= 0) {
+            if (row0 >= p.M || col >= p.N) continue;
+            if (!whole) {
                 // [column group of 8][row][8]: a warp's 32 rows are 1 KiB in a row
-                float* q = p.slots + ((it.slot * (TN / 8) + 4 * c) * TM + tile_row) * 8;
+                if (row0 + lane >= p.M) continue;
+                float* q = p.slots + ((it.slot * (TN / 8) + 4 * (part * CH + c)) * TM + (row0 - it.m_blk * TM) + lane) * 8;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     st256(q + j * TM * 8, *reinterpret_cast<uint4*>(v + 8 * j), *reinterpret_cast<uint4*>(v + 8 * j + 4));
@@ -501,8 +539,85 @@ template <int MODE, bool PAIR> __device__ void run_epilogue(const Params& p, Bar
                 }
                 continue;
             }
-            if (n0) finish16<MODE>(p, row, col, n0, v, g, ua, ub);
-            if (n1) finish16<MODE>(p, row, col + 16, n1, v + 16, g + (MODE == UP ? 16 : 0), ua + 2, ub + 2);
+            if constexpr (MODE == STORE) {
+                if (p.out_f32 || p.accumulate) {
+                    const int n0 = inside(col, p.N), n1 = inside(col + 16, p.N);
+                    if (row0 + lane < p.M) {
+                        if (n0) finish16<MODE>(p, row0 + lane, col, n0, v, g, nullptr, nullptr);
+                        if (n1) finish16<MODE>(p, row0 + lane, col + 16, n1, v + 16, g, nullptr, nullptr);
+                    }
+                    continue;
+                }
+                // boxes of 64 columns, three in turn
+                const uint32_t dst = box + (c / 2 % 3) * BOX64;
+                if (!(c & 1)) {
+                    if (lane == 0) tc::bulk_wait_read<2>();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts16(cell128(dst, lane, 4 * (c & 1) + j), pack<bf16>(v + 8 * j));
+                if ((c & 1) || col + 32 >= p.N) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_2d(&maps.out, dst, col - 32 * (c & 1), row0);
+                        tc::bulk_commit();
+                    }
+                }
+            } else if constexpr (MODE == UP) {
+                if (lane == 0) tc::bulk_wait_read<0>();
+                __syncwarp();
+                if (p.u) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sts16(cell64(box, lane, j), pack<bf16>(v + 8 * j));
+                        sts16(cell64(box + BOX32, lane, j), pack<bf16>(g + 8 * j));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = v[e] * sigmoid_fast(v[e]) * g[e];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts16(cell64(box + 2 * BOX32, lane, j), pack<bf16>(v + 8 * j));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (p.u) {
+                        tc::tma_store_2d(&maps.u_a, box, col, row0);
+                        tc::tma_store_2d(&maps.u_b, box + BOX32, col, row0);
+                    }
+                    tc::tma_store_2d(&maps.out, box + 2 * BOX32, col, row0);
+                    tc::bulk_commit();
+                }
+            } else {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(u_bar, u_phase, kWaitLimit));
+                if (!ok) {
+                    raise_abort(b, 64u);
+                    break;
+                }
+                u_phase ^= 1u;
+                u_pending = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t ca = cell64(box, lane, j), cb = cell64(box + BOX32, lane, j);
+                    float fa[8], fb[8];
+                    unpack<bf16>(lds16(ca), fa);
+                    unpack<bf16>(lds16(cb), fb);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dact_one(v[8 * j + e], fa[e], fb[e]);
+                    sts16(ca, pack<bf16>(fa));
+                    sts16(cb, pack<bf16>(fb));
+                    sts16(cell64(box + 2 * BOX32, lane, j), pack<bf16>(v + 8 * j));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::tma_store_2d(&maps.du_a, box, col, row0);
+                    tc::tma_store_2d(&maps.du_b, box + BOX32, col, row0);
+                    if (p.out) tc::tma_store_2d(&maps.out, box + 2 * BOX32, col, row0);
+                    tc::bulk_commit();
+                }
+                if (c + 1 < CH && col + 32 < p.N) fetch_u(col + 32);
+            }
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -514,16 +629,20 @@ template <int MODE, bool PAIR> __device__ void run_epilogue(const Params& p, Bar
                 tc::mbar_arrive(e);
         }
     }
+    // copies in and out of this warp's boxes end before its CTA does
+    if (MODE == DACT && u_pending && !mbar_wait_bounded(u_bar, u_phase, kWaitLimit)) atomicOr(&g_error, 64u);
+    if (lane == 0) tc::bulk_wait_all();
+    __syncwarp();
 }
 
 template <int MODE, bool A_MN, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(block_threads(MODE), 1)
-    k_product(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ Params p)
+    k_product(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    Bars* b = reinterpret_cast<Bars*>(ring + (size_t)STAGES * STAGE_BYTES);
+    uint8_t* staging = ring + (size_t)STAGES * STAGE_BYTES;
+    Bars* b = reinterpret_cast<Bars*>(staging + EPI_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t TMEM_COLS = 2 * tile_n<PAIR>();
     Where w;
@@ -543,11 +662,13 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
             mbar_init(smem_u32(&b->acc_full[i]), 1);
             mbar_init(smem_u32(&b->acc_empty[i]), (PAIR ? 2 : 1) * epi_warps(MODE));
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&b->u_full[i]), 1);
         mbar_init(smem_u32(&b->drain), 1);
         b->abort = 0;
         mbar_fence_init();
-        tc::prefetch_tmap(&tmA);
-        tc::prefetch_tmap(&tmB);
+        tc::prefetch_tmap(&maps.a);
+        tc::prefetch_tmap(&maps.b);
     }
     if (warp == 1) {
         if constexpr (PAIR) {
@@ -566,11 +687,11 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
     griddep_launch();
     griddep_wait();
     if (warp == 0) {
-        if (lane == 0) run_producer<MODE, A_MN, B_MN, PAIR>(&tmA, &tmB, p, ring, b, w);
+        if (lane == 0) run_producer<MODE, A_MN, B_MN, PAIR>(&maps.a, &maps.b, p, ring, b, w);
     } else if (warp == 1) {
         if (lane == 0 && w.rank == 0) run_mma<A_MN, B_MN, PAIR>(p, ring, b, w);
     } else {
-        run_epilogue<MODE, PAIR>(p, b, w);
+        run_epilogue<MODE, PAIR>(maps, p, smem_u32(staging), b, w);
     }
 
     tc::fence_before_sync();
@@ -693,6 +814,32 @@ bool make_map(CUtensorMap* m, const Mat& t, bool mn, int32_t rows, int32_t* both
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map of what an epilogue copies: boxes of 32 rows of `cols` columns (32 or 64).
+bool out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t width, int64_t ld, int32_t cols)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)cols, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The maps of a product's epilogue; a single row's stride counts as its width.
+bool out_maps(ffn::Maps& m, const FfnProduct& g)
+{
+    auto one = [&](CUtensorMap* t, const void* p, int64_t ld, int32_t cols) {
+        return !p || out_map(t, p, g.M, g.N, ld, cols);
+    };
+    const bf16 *u = static_cast<const bf16*>(g.u), *du = static_cast<const bf16*>(g.du);
+    if (g.epi == FFN_STORE) return g.out_f32 || g.accumulate || one(&m.out, g.out, g.ld_out, 64);
+    return one(&m.out, g.out, g.ld_out, 32) && one(&m.u_a, u, g.ld_u, 32) && one(&m.u_b, u ? u + g.N : u, g.ld_u, 32) &&
+           one(&m.du_a, du, g.ld_du, 32) && one(&m.du_b, du ? du + g.N : du, g.ld_du, 32);
+}
+
 // Tile shape of a product and how its last tiles are shared out, from its sizes alone.
 struct Plan {
     bool pair;
@@ -728,7 +875,7 @@ Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 }
 
 template <int MODE, bool A_MN, bool B_MN, bool PAIR>
-cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ffn::Params& p, bool after, cudaStream_t s)
+cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
 {
     auto kern = ffn::k_product<MODE, A_MN, B_MN, PAIR>;
     constexpr int kMaxDevices = 64;
@@ -771,15 +918,15 @@ cudaError_t launch_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const ff
     }
     workers = std::min<int64_t>(std::max<int64_t>(p.whole, p.pieces), workers);
     cfg.gridDim = dim3((unsigned)(PAIR ? 2 * workers : workers));
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, p);
+    return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
 template <int MODE, bool A_MN, bool B_MN>
-cudaError_t launch_shape(bool pair, const CUtensorMap& ma, const CUtensorMap& mb, const ffn::Params& p, bool after,
+cudaError_t launch_shape(bool pair, const ffn::Maps& maps, const ffn::Params& p, bool after,
                          cudaStream_t s)
 {
-    return pair ? launch_kernel<MODE, A_MN, B_MN, true>(ma, mb, p, after, s)
-                : launch_kernel<MODE, A_MN, B_MN, false>(ma, mb, p, after, s);
+    return pair ? launch_kernel<MODE, A_MN, B_MN, true>(maps, p, after, s)
+                : launch_kernel<MODE, A_MN, B_MN, false>(maps, p, after, s);
 }
 
 template <int MODE, bool PAIR> cudaError_t launch_join(const ffn::Params& p, cudaStream_t s)
@@ -816,14 +963,15 @@ size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 
 cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
 {
-    CUtensorMap ma, mb;
+    ffn::Maps maps;
     const Plan r = plan(g.epi, g.M, g.N, g.K);
     ffn::Params p{};
     int32_t a_rows = !r.pair && !g.a_mn && r.tiles_m == 1 ? (int32_t)((g.M + 7) / 8 * 8) : ffn::BM;
     if (a_rows == ffn::BOX) a_rows += 8;  // 64 means two boxes
     p.stage_bytes = ffn::OP_BYTES + a_rows * ffn::BK * 2;
-    if (!make_map(&ma, g.a, g.a_mn, a_rows, &p.a_blocks) ||
-        !make_map(&mb, g.b, g.b_mn, g.epi == FFN_UP && !r.pair ? ffn::BOX : ffn::BM, &p.b_blocks)) {
+    if (!make_map(&maps.a, g.a, g.a_mn, a_rows, &p.a_blocks) ||
+        !make_map(&maps.b, g.b, g.b_mn, g.epi == FFN_UP && !r.pair ? ffn::BOX : ffn::BM, &p.b_blocks) ||
+        !out_maps(maps, g)) {
         record_error("tensor map encoding failed (cuTensorMapEncodeTiled unavailable or refused the layout)");
         return cudaErrorInvalidValue;
     }
@@ -849,15 +997,15 @@ cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
              (g.epi == FFN_STORE || g.N % 16 == 0);
     cudaError_t e;
     if (g.epi == FFN_UP)
-        e = launch_shape<ffn::UP, false, false>(r.pair, ma, mb, p, after, s);
+        e = launch_shape<ffn::UP, false, false>(r.pair, maps, p, after, s);
     else if (g.epi == FFN_DACT)
-        e = launch_shape<ffn::DACT, false, true>(r.pair, ma, mb, p, after, s);
+        e = launch_shape<ffn::DACT, false, true>(r.pair, maps, p, after, s);
     else if (g.a_mn)  // dW: both operands with M, N contiguous
-        e = launch_shape<ffn::STORE, true, true>(r.pair, ma, mb, p, after, s);
+        e = launch_shape<ffn::STORE, true, true>(r.pair, maps, p, after, s);
     else if (g.b_mn)  // dx
-        e = launch_shape<ffn::STORE, false, true>(r.pair, ma, mb, p, after, s);
+        e = launch_shape<ffn::STORE, false, true>(r.pair, maps, p, after, s);
     else  // y
-        e = launch_shape<ffn::STORE, false, false>(r.pair, ma, mb, p, after, s);
+        e = launch_shape<ffn::STORE, false, false>(r.pair, maps, p, after, s);
     if (e != cudaSuccess || !r.pieces) return e;
     if (g.epi == FFN_UP) return launch_join<ffn::UP>(r.pair, p, s);
     if (g.epi == FFN_DACT) return launch_join<ffn::DACT>(r.pair, p, s);
