@@ -742,6 +742,7 @@ template <int MODE, bool PAIR> __global__ void __launch_bounds__(256) k_join(con
         const int n = inside(col, p.N);
         if (r >= rows || n == 0) continue;
         float v[16] = {}, g[16] = {};
+#pragma unroll 2
         for (int64_t w = w0; w <= w1; ++w) {
             const int64_t slot = 2 * w + (w * p.piece_kb <= first ? 1 : 0);
             const float* q = p.slots + ((slot * (TN / 8) + 2 * c) * TM + r) * 8;
@@ -848,30 +849,61 @@ struct Plan {
     int32_t pieces, piece_kb;
 };
 
+// What a shape costs, in microseconds, from runs of both shapes at some twenty sizes (d 64 to
+// 5120, width 64 to 13,824, 64 to 30,000 tokens): the launch with its first fill and last drain, a k-block with
+// few workers and with all of them busy (the copies from L2 then bound it), and the least time of
+// a tile (its epilogue).
+struct ShapeCost {
+    double launch, kb_few, kb_busy, tile;
+};
+constexpr ShapeCost kSingle{4.0, 0.25, 0.43, 1.0}, kPair{6.0, 0.31, 0.43, 2.5};
+
+// The cheaper way to share out the last tiles of a shape; returns the product's cost.
+double share_out(Plan& r, const ShapeCost& c, int64_t workers, double slot_mb)
+{
+    const auto kb_time = [&](int64_t active) { return std::max(c.kb_few, c.kb_busy * (double)active / (double)workers); };
+    const int64_t rest = r.tiles % workers, q = rest * r.kblocks;
+    r.whole = r.tiles;
+    r.pieces = r.piece_kb = 0;
+    double cost = c.launch + (double)(r.tiles / workers) * std::max(r.kblocks * c.kb_busy, c.tile);
+    if (!rest) return cost;
+    double best = r.kblocks * kb_time(rest) + c.tile;
+    const int64_t least = (q + workers - 1) / workers;
+    for (int s = 2; s <= 32 && s <= r.kblocks; ++s) {
+        const int64_t kb = std::max<int64_t>(least, (r.kblocks + s - 1) / s), pieces = (q + kb - 1) / kb;
+        // the join: its launch, a tile's pieces one after another, the slots written and read
+        const double join = 3.0 + 0.15 * (double)((pieces + rest - 1) / rest) + 2.0 * slot_mb * (double)pieces / 5.0;
+        const double t = (double)kb * kb_time(pieces) + c.tile + join;
+        if (t < best) {
+            best = t;
+            r.whole = r.tiles - rest;
+            r.pieces = (int32_t)pieces;
+            r.piece_kb = (int32_t)kb;
+        }
+    }
+    return cost + best;
+}
+
 Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 {
-    Plan r{};
-    r.pair = M > ffn::BM;
-    const int64_t tm = r.pair ? 256 : 128, tn = epi == FFN_UP ? tm / 2 : tm;
-    const int64_t workers = r.pair ? ffn::B200_SMS / 2 : ffn::B200_SMS;
-    r.kblocks = (int32_t)((K + ffn::BK - 1) / ffn::BK);
-    r.tiles_m = (int32_t)((M + tm - 1) / tm);
-    r.tiles_n = (int32_t)((N + tn - 1) / tn);
-    r.tiles = r.whole = (int64_t)r.tiles_m * r.tiles_n;
-    const int64_t rest = r.tiles % workers, q = rest * r.kblocks;
-    if (!rest) return r;
-    // microseconds: a k-block of a tile with every worker busy; the join's launch; the pieces written
-    // and read back
-    const double t_kb = r.pair ? 0.3 : 0.35;
-    const int64_t most = std::min<int64_t>(workers, std::max<int64_t>(q / 4, 1));  // at least four k-blocks a piece
-    const int64_t kb = (q + most - 1) / most, pieces = (q + kb - 1) / kb;
-    const double area = (double)std::min(M, tm) * (double)(r.pair ? 256 : 128) * 4e-6;  // MB of a slot
-    const double join = 3.0 + 2.0 * area * (double)(pieces + rest) / 6.0;
-    if ((double)(r.kblocks - kb) * t_kb <= join) return r;
-    r.whole = r.tiles - rest;
-    r.pieces = (int32_t)pieces;
-    r.piece_kb = (int32_t)kb;
-    return r;
+    Plan best{};
+    double cost = 0;
+    for (int pair = 0; pair < (M > ffn::BM ? 2 : 1); ++pair) {
+        Plan r{};
+        r.pair = pair;
+        const int64_t tm = pair ? 256 : 128, tn = epi == FFN_UP ? tm / 2 : tm;
+        r.kblocks = (int32_t)((K + ffn::BK - 1) / ffn::BK);
+        r.tiles_m = (int32_t)((M + tm - 1) / tm);
+        r.tiles_n = (int32_t)((N + tn - 1) / tn);
+        r.tiles = (int64_t)r.tiles_m * r.tiles_n;
+        const double slot_mb = (double)std::min(M, tm) * (double)tm * 4e-6;
+        const double c = share_out(r, pair ? kPair : kSingle, pair ? ffn::B200_SMS / 2 : ffn::B200_SMS, slot_mb);
+        if (!pair || c < cost) {
+            best = r;
+            cost = c;
+        }
+    }
+    return best;
 }
 
 template <int MODE, bool A_MN, bool B_MN, bool PAIR>
