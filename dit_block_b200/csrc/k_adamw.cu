@@ -20,9 +20,7 @@ namespace adamw {
 constexpr int THREADS = 256;
 constexpr int BLOCK = SOL_ADAMW_BLOCK;
 constexpr int CHUNK = kAdamwChunk;
-#ifndef STEP8_CTAS
-#define STEP8_CTAS 4
-#endif
+constexpr int STEP8_CTAS = 3;         // 80 registers: no spills (4 CTAs of 64 registers: 1077 against 1060 us)
 constexpr int NORM_CTAS = 148 * 8;  // partial sums of the gradient norm
 static_assert((NORM_CTAS) * sizeof(double) <= SOL_ADAMW_NORM_WORKSPACE, "the norm's partial sums must fit its workspace");
 
@@ -172,17 +170,23 @@ __device__ __forceinline__ float2 decode_unit(float s, float step)
     return s < 1e-28f ? make_float2(step, s) : make_float2(step * s, 1.f);
 }
 // k * |k| and k^4 are formed with at most one rounding, the products add three more
-__device__ __forceinline__ float2 decode_first2(float2 z, float2 u)  // z: 2^23 + (code ^ 0x80)
+__device__ __forceinline__ float2 decode_first2(float2 z, float u)  // z: 2^23 + (code ^ 0x80)
 {
     const float2 k = __fadd2_rn(z, both(-(8388608.f + 128.f)));
-    return __fmul2_rn(__fmul2_rn(make_float2(k.x * fabsf(k.x), k.y * fabsf(k.y)), both(u.x)), both(u.y));
+    return __fmul2_rn(make_float2(k.x * fabsf(k.x), k.y * fabsf(k.y)), both(u));
 }
-__device__ __forceinline__ float2 decode_second2(float2 z, float2 u)  // z: 2^23 + code
+__device__ __forceinline__ float2 decode_second2(float2 z, float u)  // z: 2^23 + code
 {
     const float2 k = __fadd2_rn(z, both(-8388608.f)), k2 = __fmul2_rn(k, k);
-    return __fmul2_rn(__fmul2_rn(__fmul2_rn(k2, k2), both(u.x)), both(u.y));
+    return __fmul2_rn(__fmul2_rn(k2, k2), both(u));
 }
 constexpr float STEP1 = 1.f / 16129.f, STEP2 = (float)(1.0 / 4228250625.0);  // 127^-2, 255^-4
+
+__device__ __forceinline__ void scale8(float2* x, float f)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(x[e], both(f));
+}
 
 // Eight codes (two words) of a block to values.
 __device__ __forceinline__ void decode_first8(uint2 q, float s, float2* m)
@@ -191,8 +195,9 @@ __device__ __forceinline__ void decode_first8(uint2 q, float s, float2* m)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const uint32_t w = (e < 2 ? q.x : q.y) ^ 0x80808080u;
-        m[e] = decode_first2(make_float2(magic_byte(w, 2 * (e & 1)), magic_byte(w, 2 * (e & 1) + 1)), u);
+        m[e] = decode_first2(make_float2(magic_byte(w, 2 * (e & 1)), magic_byte(w, 2 * (e & 1) + 1)), u.x);
     }
+    if (u.y != 1.f) scale8(m, u.y);
 }
 __device__ __forceinline__ void decode_second8(uint2 q, float s, float2* v)
 {
@@ -200,8 +205,9 @@ __device__ __forceinline__ void decode_second8(uint2 q, float s, float2* v)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const uint32_t w = e < 2 ? q.x : q.y;
-        v[e] = decode_second2(make_float2(magic_byte(w, 2 * (e & 1)), magic_byte(w, 2 * (e & 1) + 1)), u);
+        v[e] = decode_second2(make_float2(magic_byte(w, 2 * (e & 1)), magic_byte(w, 2 * (e & 1) + 1)), u.x);
     }
+    if (u.y != 1.f) scale8(v, u.y);
 }
 
 __device__ __forceinline__ float root_ftz(float x)
@@ -318,23 +324,15 @@ __device__ __forceinline__ Unit unit_of(float s, float most)
 {
     Unit u;
     u.pre = s < 1e-28f ? 1.2676506e30f : 1.f;
-    u.inv = s > 0.f ? most / (s * u.pre) : 0.f;
+    u.inv = s > 0.f ? most * rcp_ftz(s * u.pre) : 0.f;  // off by 2^-22: the margin of 2^-20 covers it
     return u;
 }
-__device__ __forceinline__ void scale8(float2* x, float f)
-{
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(x[e], both(f));
-}
-
-// Everything that a lane does with its eight values of a block, all from registers.
-template <bool ROOT_FTZ>
-__device__ __forceinline__ void step_lane(float2* p, float2* m, float2* v, const float2* g, uint32_t at, int live, float wd,
-                                          const Scalars& h, const Live& l, uint2& q1, uint2& q2, float& n1, float& n2)
+// The codes of a lane's eight new moments and the scales of their block; values from `live` on
+// lie behind the tensor's end.
+__device__ __forceinline__ void encode8(float2* m, float2* v, uint32_t at, int live, uint2& q1, uint2& q2, float& n1,
+                                        float& n2)
 {
     float top1 = 0.f, top2 = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) update2<ROOT_FTZ>(p[e], m[e], v[e], g[e], -l.lr * l.inv_bc1, -l.lr * wd, h, l);
     if (live < 8) {  // values past the tensor's end count for nothing
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -397,6 +395,7 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
     uint8_t *pm = static_cast<uint8_t*>(x.m), *pv = static_cast<uint8_t*>(x.v);
     bf16* copy = static_cast<bf16*>(x.copy);
     const uint32_t key = mixed(mixed(mixed(x.ordinal * 0x9E3779B9u + l.step) ^ h.seed_hi) ^ h.seed_lo);
+    const uint32_t from = mixed(key + (uint32_t)((uint64_t)c.index * CHUNK >> 32));  // a chunk's upper halves agree
     const int64_t base = (int64_t)c.index * CHUNK, end = min(x.n, base + CHUNK);
     int64_t start = base + warp * BLOCK;
     constexpr int STRIDE = THREADS / 32 * BLOCK;
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
             s1 = x.ms[blk + THREADS / 32];
             s2 = x.vs[blk + THREADS / 32];
         }
-        const uint32_t at = mixed(key + (uint32_t)((uint64_t)start >> 32)) + (uint32_t)i;
+        const uint32_t at = from + (uint32_t)i;
         float2 p[4], g[4], m[4], v[4];
         uint2 q1, q2;
         if (start + BLOCK <= end) {
@@ -440,12 +439,15 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
             if (sizeof(G) == 4) unpack2<G>(*reinterpret_cast<const uint4*>(d.g + 4), g + 2);
             decode_first8(d.m, n1, m);
             decode_second8(d.v, n2, v);
-            step_lane<ROOT_FTZ>(p, m, v, g, at, 8, x.wd, h, l, q1, q2, n1, n2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) update2<ROOT_FTZ>(p[e], m[e], v[e], g[e], -l.lr * l.inv_bc1, -l.lr * x.wd, h, l);
+            // the parameters leave first: their registers are free for the codes
             st_stream(x.p + i, pack2<float>(p));
             st_stream(x.p + i + 4, pack2<float>(p + 2));
+            if (copy) st_stream(copy + i, pack2<bf16>(p));
+            encode8(m, v, at, 8, q1, q2, n1, n2);
             *reinterpret_cast<uint2*>(pm + i) = q1;
             *reinterpret_cast<uint2*>(pv + i) = q2;
-            if (copy) st_stream(copy + i, pack2<bf16>(p));
         } else {
             // the tensor's last block
             const int live = (int)min((int64_t)8, max((int64_t)0, x.n - i));
@@ -464,7 +466,9 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
             }
             decode_first8(make_uint2(w1[0], w1[1]), n1, m);
             decode_second8(make_uint2(w2[0], w2[1]), n2, v);
-            step_lane<ROOT_FTZ>(p, m, v, g, at, live, x.wd, h, l, q1, q2, n1, n2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) update2<ROOT_FTZ>(p[e], m[e], v[e], g[e], -l.lr * l.inv_bc1, -l.lr * x.wd, h, l);
+            encode8(m, v, at, live, q1, q2, n1, n2);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (e < live) {
