@@ -48,10 +48,6 @@ constexpr int BK = 64;                     // K per stage
 constexpr int UK = 16;                     // K of one tcgen05.mma
 constexpr int BOX = 64;                    // a box is BOX x BOX
 constexpr int BOX_BYTES = BOX * BOX * 2;   // 8 KiB
-constexpr int OP_BYTES = 2 * BOX_BYTES;    // one operand of a stage
-constexpr int STAGE_BYTES = 2 * OP_BYTES;  // 32 KiB
-constexpr int STAGES = 5;                  // as fast as 6 and 7, and leaves room for the epilogue
-constexpr int EPI_BYTES = 49152;           // staging of the epilogue warps
 // m-blocks per raster group: 74 pairs then work on 8 x 9 tiles at a time, which read the fewest
 // distinct rows of A and B.  DRAM reads of dx and dW_up at 31,248 tokens 13.4 GB each, 14.4 (and up
 // to 25) with 16, 19 with 4; the whole backward pass 21.6 against 22.5 ms at the power cap.
@@ -63,22 +59,45 @@ constexpr int B200_SMS = 148;              // plan() is a function of the sizes 
 
 enum Mode : int { STORE = FFN_STORE, UP = FFN_UP, DACT = FFN_DACT };
 
-template <bool PAIR> __host__ __device__ constexpr int tile_m() { return PAIR ? 2 * BM : BM; }
-template <bool PAIR> __host__ __device__ constexpr int tile_n() { return PAIR ? 256 : 128; }
+// Tile shapes:
+//   SINGLE  one CTA, 128 x 128, two accumulators in TMEM;
+//   PAIR    two CTAs on two SMs, 256 x 256 (256-row MMAs, each CTA loading half of A and half of
+//           B), two accumulators, so that the epilogue of a tile runs under the next tile;
+//   WIDE    the same pair on 512 x 256: two MMAs a step share B, a quarter less comes from L2
+//           than by two PAIR tiles (which bound PAIR: 64 KiB a k-block and pair, 11 TB/s in
+//           all); the accumulators fill TMEM, so that the epilogue stands between two tiles.
+enum Shape : int { SINGLE = 0, PAIR = 1, WIDE = 2 };
+template <int S> struct Tile {
+    static constexpr bool PAIRED = S != SINGLE;
+    static constexpr int HALVES = S == WIDE ? 2 : 1;  // 128-row halves of A a CTA holds
+    static constexpr int ROWS = BM * HALVES;          // rows of a CTA
+    static constexpr int M = PAIRED ? 2 * ROWS : ROWS, N = PAIRED ? 256 : 128;
+    static constexpr int A_BYTES = ROWS * BK * 2, STAGE_BYTES = A_BYTES + 128 * BK * 2;
+    static constexpr int STAGES = S == WIDE ? 4 : 5;  // PAIR: as fast as 6 and 7
+    static constexpr int EPI_BYTES = S == WIDE ? 32768 : 49152;  // staging of the epilogue warps
+    static constexpr int ACCS = S == WIDE ? 1 : 2;    // accumulators in TMEM
+    static constexpr int TMEM_COLS = S == SINGLE ? 256 : 512;
+};
+constexpr int MAX_STAGES = 5;
 
 // Epilogue warps: four (one per TMEM lane quarter) where the epilogue only stores, eight
-// where it also computes (two per quarter, half of the columns each).
-__host__ __device__ constexpr int epi_warps(int mode) { return mode == UP || mode == DACT ? 8 : 4; }
-__host__ __device__ constexpr int block_threads(int mode) { return 64 + 32 * epi_warps(mode); }
+// where it also computes (two per quarter, half of the columns each) or holds up the MMAs (two
+// per quarter, half of the rows each).
+__host__ __device__ constexpr int epi_warps(int mode, int shape) { return mode != STORE || shape == WIDE ? 8 : 4; }
+__host__ __device__ constexpr int block_threads(int mode, int shape) { return 64 + 32 * epi_warps(mode, shape); }
 
 struct Bars {
-    uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drain;
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drain;
     uint64_t u_full[8];         // DACT: a warp's pieces of u have landed
-    int32_t peer_last[STAGES];  // leader: phase of the peer's last copy per stage (-1: none)
+    int32_t peer_last[MAX_STAGES];  // leader: phase of the peer's last copy per stage (-1: none)
     uint32_t tmem_base;
     volatile int32_t abort;
 };
-constexpr size_t kSmemBytes = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + sizeof(Bars);
+template <int S> constexpr size_t smem_bytes()
+{
+    return 1024 + (size_t)Tile<S>::STAGES * Tile<S>::STAGE_BYTES + Tile<S>::EPI_BYTES + sizeof(Bars);
+}
+static_assert(smem_bytes<WIDE>() <= 232448 && smem_bytes<PAIR>() <= 232448, "shared memory of a CTA");
 
 __device__ uint32_t g_error;
 
@@ -88,7 +107,7 @@ struct Params {
     int64_t whole, tiles;        // tiles [0, whole) are worked on whole, one after another by each worker
     int32_t pieces, piece_kb;    // tiles [whole, tiles): their K end to end in `pieces` of piece_kb blocks
     int32_t stage_bytes;         // bytes that the copies of one CTA and stage bring
-    int32_t a_blocks, b_blocks;  // 1: a copy brings both 64-row halves of the operand (see make_map)
+    int32_t a_blocks, b_blocks;  // 1: one copy brings a CTA's rows of the operand (see make_map)
     int32_t out_f32, accumulate;
     int32_t wide;                // rows of out, u and du (and their second halves) begin on 32-byte boundaries
     void* out;
@@ -126,12 +145,11 @@ struct Piece {
 // worked on at one time share rows of A and of B in L2.
 __device__ __forceinline__ void tile_at(int64_t t, const Params& p, int32_t& m_blk, int32_t& n_blk)
 {
-    const int64_t per_group = (int64_t)GROUP_M * p.tiles_n;
-    const int32_t g = (int32_t)(t / per_group);
-    const int32_t gm = min(GROUP_M, p.tiles_m - g * GROUP_M);
-    const int32_t local = (int32_t)(t - g * per_group);
-    m_blk = g * GROUP_M + local % gm;
-    n_blk = local / gm;
+    const uint32_t per_group = GROUP_M * (uint32_t)p.tiles_n, g = (uint32_t)t / per_group;  // tiles: below 2^31
+    const uint32_t gm = min((uint32_t)GROUP_M, (uint32_t)p.tiles_m - g * GROUP_M);
+    const uint32_t local = (uint32_t)t - g * per_group;
+    m_blk = (int32_t)(g * GROUP_M + local % gm);
+    n_blk = (int32_t)(local / gm);
 }
 
 // The pieces of one worker, the same sequence for every role: whole tiles, then its share of
@@ -177,11 +195,11 @@ struct Where {
     int64_t worker, n_workers;
 };
 
-template <bool PAIR> __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, Bars* b)
+template <bool PAIRED> __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, Bars* b)
 {
-    const uint32_t limit = PAIR ? kPollLimit : kWaitLimit;
+    const uint32_t limit = PAIRED ? kPollLimit : kWaitLimit;
     for (uint32_t i = 0; i < limit; ++i) {
-        if (PAIR ? tc::mbar_poll_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (PAIRED ? tc::mbar_poll_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 15u) == 15u && b->abort) return false;
     }
     return false;
@@ -193,9 +211,9 @@ __device__ __forceinline__ void raise_abort(Bars* b, uint32_t code)
     atomicOr(&g_error, code);
 }
 
-// The 128 rows of one operand, [x0, x0 + 64) and [x1, x1 + 64), for the 64 K from k on.  One copy
-// where the map's box holds both halves, else two.
-template <bool MN>
+// A CTA's rows of one operand, BOXES times 64 of them ([x0, x0 + 64), [x1, x1 + 64), then on from x0 + 128),
+// for the 64 K from k on: one copy where the map's box holds them all, else one for each 64.
+template <bool MN, int BOXES>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int32_t form, int32_t x0, int32_t x1,
                                              int32_t k, uint32_t bar, bool remote)
 {
@@ -203,21 +221,25 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
         remote ? tc::tma_load_3d_pair(dst, map, 0, k, x0 / BOX, bar) : tc::tma_load_3d(dst, map, 0, k, x0 / BOX, bar);
         return;
     }
-    const int32_t c0 = MN ? x0 : k, r0 = MN ? k : x0, c1 = MN ? x1 : k, r1 = MN ? k : x1;
-    remote ? tc::tma_load_2d_pair(dst, map, c0, r0, bar) : tc::tma_load_2d(dst, map, c0, r0, bar);
-    if (form) return;
-    remote ? tc::tma_load_2d_pair(dst + BOX_BYTES, map, c1, r1, bar) : tc::tma_load_2d(dst + BOX_BYTES, map, c1, r1, bar);
+#pragma unroll
+    for (int i = 0; i < BOXES; ++i) {
+        const int32_t x = i == 1 ? x1 : x0 + i * BOX, c = MN ? x : k, r = MN ? k : x;
+        remote ? tc::tma_load_2d_pair(dst + i * BOX_BYTES, map, c, r, bar) : tc::tma_load_2d(dst + i * BOX_BYTES, map, c, r, bar);
+        if (form) return;
+    }
 }
 
 // Producer (one thread per CTA): this CTA's 128 rows of A and its 128 rows of B (64 of the
 // gated half and 64 of the other for UP in the single shape; in a pair the leader loads the
 // gated half, the peer the other).  The peer's copies complete on the leader's barrier,
 // which the leader armed for both CTAs' bytes.
-template <int MODE, bool A_MN, bool B_MN, bool PAIR>
+template <int MODE, bool A_MN, bool B_MN, int S>
 __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, const Params& p, uint8_t* ring, Bars* b,
                              const Where& w)
 {
-    const bool remote = PAIR && w.rank == 1;
+    using T = Tile<S>;
+    constexpr int STAGES = T::STAGES;
+    const bool remote = T::PAIRED && w.rank == 1;
     int s = 0;
     uint32_t phase = 0;
     int32_t last[STAGES];
@@ -226,10 +248,10 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
     Walk walk = walk_begin(w.worker);
     Piece it;
     while (!b->abort && walk_next(walk, p, w.n_workers, it)) {
-        const int32_t ma = it.m_blk * tile_m<PAIR>() + (int32_t)w.rank * BM;
+        const int32_t ma = it.m_blk * T::M + (int32_t)w.rank * T::ROWS;
         int32_t n0, n1;
         if (MODE == UP) {
-            if (PAIR) {
+            if (T::PAIRED) {
                 n0 = it.n_blk * 128 + (w.rank ? p.N : 0);
                 n1 = n0 + BOX;
             } else {
@@ -237,22 +259,22 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
                 n1 = p.N + n0;
             }
         } else {
-            n0 = it.n_blk * tile_n<PAIR>() + (int32_t)w.rank * 128;
+            n0 = it.n_blk * T::N + (int32_t)w.rank * 128;
             n1 = n0 + BOX;
         }
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
-            if (!wait_or_abort<PAIR>(smem_u32(&b->empty[s]), phase ^ 1u, b)) {
+            if (!wait_or_abort<T::PAIRED>(smem_u32(&b->empty[s]), phase ^ 1u, b)) {
                 raise_abort(b, 1u);
                 break;
             }
-            const uint32_t dst = smem_u32(ring + (size_t)s * STAGE_BYTES);
+            const uint32_t dst = smem_u32(ring + (size_t)s * T::STAGE_BYTES);
             uint32_t bar = smem_u32(&b->full[s]);
             if (remote)
                 bar = tc::mapa(bar, 0);
             else
-                mbar_arrive_expect_tx(bar, PAIR ? 2 * p.stage_bytes : p.stage_bytes);
-            load_operand<A_MN>(dst, tmA, p.a_blocks, ma, ma + BOX, kb * BK, bar, remote);
-            load_operand<B_MN>(dst + OP_BYTES, tmB, p.b_blocks, n0, n1, kb * BK, bar, remote);
+                mbar_arrive_expect_tx(bar, T::PAIRED ? 2 * p.stage_bytes : p.stage_bytes);
+            load_operand<A_MN, T::ROWS / BOX>(dst, tmA, p.a_blocks, ma, ma + BOX, kb * BK, bar, remote);
+            load_operand<B_MN, 2>(dst + T::A_BYTES, tmB, p.b_blocks, n0, n1, kb * BK, bar, remote);
             last[s] = (int32_t)phase;
             if (++s == STAGES) {
                 s = 0;
@@ -274,67 +296,76 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
 }
 
 // MMA issuer (one thread; the leader's in a pair).
-template <bool A_MN, bool B_MN, bool PAIR>
+template <bool A_MN, bool B_MN, int S>
 __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
 {
-    const uint32_t idesc = tc::idesc_bf16_f32(tile_m<PAIR>(), tile_n<PAIR>()) | (A_MN ? 1u << 15 : 0u) |
+    using T = Tile<S>;
+    const uint32_t idesc = tc::idesc_bf16_f32(T::PAIRED ? 2 * BM : BM, T::N) | (A_MN ? 1u << 15 : 0u) |
                            (B_MN ? 1u << 16 : 0u);
     // UK elements of K further: 32 bytes inside a swizzled row, or two 8-row atoms
     constexpr uint64_t A_STEP = A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = B_MN ? 2048 >> 4 : 32 >> 4;
+    constexpr uint64_t A_HALF = BM * BK * 2 >> 4;
     int s = 0;
     uint32_t phase = 0;
     int64_t n = 0;
     Walk walk = walk_begin(w.worker);
-    Piece it;
-    for (; !b->abort && walk_next(walk, p, w.n_workers, it); ++n) {
-        const int ab = (int)(n & 1);
-        if (!wait_or_abort<PAIR>(smem_u32(&b->acc_empty[ab]), (uint32_t)((n >> 1) & 1) ^ 1u, b)) {
+    Piece next;
+    bool more = walk_next(walk, p, w.n_workers, next);
+    for (; more && !b->abort; ++n) {
+        const Piece it = next;
+        const int ab = T::ACCS == 2 ? (int)(n & 1) : 0;
+        const uint32_t acc_phase = (uint32_t)(T::ACCS == 2 ? n >> 1 : n) & 1u;
+        if (!wait_or_abort<T::PAIRED>(smem_u32(&b->acc_empty[ab]), acc_phase ^ 1u, b)) {
             raise_abort(b, 4u);
             break;
         }
         tc::fence_after_sync();
-        const uint32_t d = b->tmem_base + (uint32_t)(ab * tile_n<PAIR>());
+        const uint32_t d = b->tmem_base + (uint32_t)(ab * T::N);
         bool ok = true;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
-            if (!wait_or_abort<PAIR>(smem_u32(&b->full[s]), phase, b)) {
+            if (!wait_or_abort<T::PAIRED>(smem_u32(&b->full[s]), phase, b)) {
                 raise_abort(b, 8u);
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t a_addr = smem_u32(ring + (size_t)s * STAGE_BYTES), b_addr = a_addr + OP_BYTES;
+            const uint32_t a_addr = smem_u32(ring + (size_t)s * T::STAGE_BYTES), b_addr = a_addr + T::A_BYTES;
             const uint64_t a_desc = A_MN ? smem_desc_mn(a_addr) : tc::smem_desc_sw128(a_addr);
             const uint64_t b_desc = B_MN ? smem_desc_mn(b_addr) : tc::smem_desc_sw128(b_addr);
 #pragma unroll
             for (int kk = 0; kk < BK / UK; ++kk) {
                 const uint32_t acc = (kb > it.kb0 || kk) ? 1u : 0u;
-                if (PAIR)
-                    tc::mma_bf16_pair(d, a_desc + kk * A_STEP, b_desc + kk * B_STEP, idesc, acc);
-                else
-                    tc::mma_bf16(d, a_desc + kk * A_STEP, b_desc + kk * B_STEP, idesc, acc);
+#pragma unroll
+                for (int h = 0; h < T::HALVES; ++h) {
+                    if (T::PAIRED)
+                        tc::mma_bf16_pair(d + h * T::N, a_desc + h * A_HALF + kk * A_STEP, b_desc + kk * B_STEP, idesc, acc);
+                    else
+                        tc::mma_bf16(d, a_desc + kk * A_STEP, b_desc + kk * B_STEP, idesc, acc);
+                }
             }
             const uint32_t e = smem_u32(&b->empty[s]);
-            if (PAIR) {
+            if (T::PAIRED) {
                 tc::commit_pair(e);
                 tc::commit_pair(tc::mapa(e, 1));
             } else {
                 tc::commit(e);
             }
-            if (++s == STAGES) {
+            if (++s == T::STAGES) {
                 s = 0;
                 phase ^= 1u;
             }
+            if (kb == it.kb0) more = walk_next(walk, p, w.n_workers, next);  // while the MMAs run
         }
         if (!ok) break;
         const uint32_t f = smem_u32(&b->acc_full[ab]);
-        if (PAIR) {
+        if (T::PAIRED) {
             tc::commit_pair(f);
             tc::commit_pair(tc::mapa(f, 1));
         } else {
             tc::commit(f);
         }
     }
-    if (PAIR)
+    if (T::PAIRED)
         tc::commit_pair(smem_u32(&b->drain));
     else
         tc::commit(smem_u32(&b->drain));
@@ -480,15 +511,19 @@ constexpr int BOX32 = 32 * 64, BOX64 = 32 * 128;
 // them.  (Straight from registers a warp's store touched 32 rows; at d 1000, width 2504, 4,099
 // tokens, d_act took 83 us.)  DACT brings u the same way, the first piece of a tile while its
 // product still runs.
-template <int MODE, bool PAIR>
+template <int MODE, int S>
 __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging, Bars* b, const Where& w)
 {
-    constexpr int EW = epi_warps(MODE), H = EW / 4, TN = tile_n<PAIR>(), TM = tile_m<PAIR>();
+    using T = Tile<S>;
+    constexpr int EW = epi_warps(MODE, S), TN = T::N, TM = T::M;
+    constexpr int H = EW / 4 / T::HALVES;            // warps that share a row's columns
     constexpr int WIDTH = MODE == UP ? TN / 2 : TN;  // UP: a in columns [0, WIDTH), b behind them
     constexpr int CH = WIDTH / 32 / H;               // steps of 32 columns of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quarter = warp & 3, part = (warp - EPI_WARP0) / 4;
-    const uint32_t box = staging + (warp - EPI_WARP0) * (EPI_BYTES / EW);
+    const int quarter = warp & 3, group = (warp - EPI_WARP0) / 4;
+    const int half = T::HALVES == 2 ? group : 0, part = T::HALVES == 2 ? 0 : group;
+    constexpr int SPACE = T::EPI_BYTES / EW;  // staging of a warp
+    const uint32_t box = staging + (warp - EPI_WARP0) * SPACE;
     const uint32_t u_bar = smem_u32(&b->u_full[(warp - EPI_WARP0) & 7]);
     uint32_t u_phase = 0;
     bool u_pending = false, ok = true;
@@ -496,8 +531,9 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
     Walk walk = walk_begin(w.worker);
     Piece it;
     for (; ok && walk_next(walk, p, w.n_workers, it); ++n) {
-        const int ab = (int)(n & 1);
-        const int32_t row0 = it.m_blk * TM + (int32_t)w.rank * BM + quarter * 32;  // of this warp
+        const int ab = T::ACCS == 2 ? (int)(n & 1) : 0;
+        const uint32_t acc_phase = (uint32_t)(T::ACCS == 2 ? n >> 1 : n) & 1u;
+        const int32_t row0 = it.m_blk * TM + (int32_t)w.rank * T::ROWS + half * BM + quarter * 32;  // of this warp
         const int32_t col0 = it.n_blk * WIDTH + part * CH * 32;
         const bool whole = it.slot < 0;
         auto fetch_u = [&](int32_t col) {  // lane 0, once the boxes are free
@@ -510,13 +546,13 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
             u_pending = true;
         };
         if (MODE == DACT && whole && row0 < p.M && col0 < p.N) fetch_u(col0);
-        const bool got = wait_or_abort<PAIR>(smem_u32(&b->acc_full[ab]), (uint32_t)((n >> 1) & 1), b);
+        const bool got = wait_or_abort<T::PAIRED>(smem_u32(&b->acc_full[ab]), acc_phase, b);
         if (!__all_sync(0xffffffffu, got)) {
             raise_abort(b, 32u);
             break;
         }
         tc::fence_after_sync();
-        const uint32_t t = b->tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ab * TN) + part * CH * 32;
+        const uint32_t t = b->tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ab * TN + half * TN + part * CH * 32);
         float v[32], g[MODE == UP ? 32 : 1];
 #pragma unroll 1
         for (int c = 0; c < CH && ok; ++c) {
@@ -548,10 +584,11 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                     }
                     continue;
                 }
-                // boxes of 64 columns, three in turn
-                const uint32_t dst = box + (c / 2 % 3) * BOX64;
+                // boxes of 64 columns in turn
+                constexpr int BOXES = SPACE / BOX64;
+                const uint32_t dst = box + (c / 2 % BOXES) * BOX64;
                 if (!(c & 1)) {
-                    if (lane == 0) tc::bulk_wait_read<2>();
+                    if (lane == 0) tc::bulk_wait_read<BOXES - 1>();
                     __syncwarp();
                 }
 #pragma unroll
@@ -563,6 +600,42 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                         tc::tma_store_2d(&maps.out, dst, col - 32 * (c & 1), row0);
                         tc::bulk_commit();
                     }
+                }
+            } else if constexpr (MODE == UP && SPACE < 3 * BOX32) {
+                // two boxes: a and b, then act in the first of them; act alone takes them in turn
+                if (p.u) {
+                    if (lane == 0) tc::bulk_wait_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sts16(cell64(box, lane, j), pack<bf16>(v + 8 * j));
+                        sts16(cell64(box + BOX32, lane, j), pack<bf16>(g + 8 * j));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_2d(&maps.u_a, box, col, row0);
+                        tc::tma_store_2d(&maps.u_b, box + BOX32, col, row0);
+                        tc::bulk_commit();
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = v[e] * sigmoid_fast(v[e]) * g[e];
+                const uint32_t dst = p.u ? box : box + (c & 1) * BOX32;
+                if (lane == 0) {
+                    if (p.u)
+                        tc::bulk_wait_read<0>();
+                    else
+                        tc::bulk_wait_read<1>();
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts16(cell64(dst, lane, j), pack<bf16>(v + 8 * j));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::tma_store_2d(&maps.out, dst, col, row0);
+                    tc::bulk_commit();
                 }
             } else if constexpr (MODE == UP) {
                 if (lane == 0) tc::bulk_wait_read<0>();
@@ -623,7 +696,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
         __syncwarp();
         if (lane == 0) {
             const uint32_t e = smem_u32(&b->acc_empty[ab]);
-            if (PAIR)
+            if (T::PAIRED)
                 tc::mbar_arrive_cluster(tc::mapa(e, 0));
             else
                 tc::mbar_arrive(e);
@@ -635,24 +708,24 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
     __syncwarp();
 }
 
-template <int MODE, bool A_MN, bool B_MN, bool PAIR>
-__global__ void __launch_bounds__(block_threads(MODE), 1)
+template <int MODE, bool A_MN, bool B_MN, int S>
+__global__ void __launch_bounds__(block_threads(MODE, S), 1)
     k_product(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 {
+    using T = Tile<S>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* staging = ring + (size_t)STAGES * STAGE_BYTES;
-    Bars* b = reinterpret_cast<Bars*>(staging + EPI_BYTES);
+    uint8_t* staging = ring + (size_t)T::STAGES * T::STAGE_BYTES;
+    Bars* b = reinterpret_cast<Bars*>(staging + T::EPI_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr uint32_t TMEM_COLS = 2 * tile_n<PAIR>();
     Where w;
-    w.rank = PAIR ? tc::cluster_rank() : 0u;
-    w.worker = PAIR ? blockIdx.x / 2 : blockIdx.x;
-    w.n_workers = PAIR ? gridDim.x / 2 : gridDim.x;
+    w.rank = T::PAIRED ? tc::cluster_rank() : 0u;
+    w.worker = T::PAIRED ? blockIdx.x / 2 : blockIdx.x;
+    w.n_workers = T::PAIRED ? gridDim.x / 2 : gridDim.x;
 
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < T::STAGES; ++i) {
             mbar_init(smem_u32(&b->full[i]), 1);
             mbar_init(smem_u32(&b->empty[i]), 1);
             b->peer_last[i] = -1;
@@ -660,7 +733,7 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&b->acc_full[i]), 1);
-            mbar_init(smem_u32(&b->acc_empty[i]), (PAIR ? 2 : 1) * epi_warps(MODE));
+            mbar_init(smem_u32(&b->acc_empty[i]), (T::PAIRED ? 2 : 1) * epi_warps(MODE, S));
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&b->u_full[i]), 1);
@@ -671,36 +744,36 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
         tc::prefetch_tmap(&maps.b);
     }
     if (warp == 1) {
-        if constexpr (PAIR) {
-            tc::tmem_alloc_pair(smem_u32(&b->tmem_base), TMEM_COLS);
+        if constexpr (T::PAIRED) {
+            tc::tmem_alloc_pair(smem_u32(&b->tmem_base), T::TMEM_COLS);
             tc::tmem_relinquish_pair();
         } else {
-            tc::tmem_alloc(smem_u32(&b->tmem_base), TMEM_COLS);
+            tc::tmem_alloc(smem_u32(&b->tmem_base), T::TMEM_COLS);
             tc::tmem_relinquish();
         }
     }
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (PAIR) tc::cluster_sync();  // both CTAs' barriers exist before any remote arrival
+    if constexpr (T::PAIRED) tc::cluster_sync();  // both CTAs' barriers exist before any remote arrival
     tc::fence_after_sync();
 
     griddep_launch();
     griddep_wait();
     if (warp == 0) {
-        if (lane == 0) run_producer<MODE, A_MN, B_MN, PAIR>(&maps.a, &maps.b, p, ring, b, w);
+        if (lane == 0) run_producer<MODE, A_MN, B_MN, S>(&maps.a, &maps.b, p, ring, b, w);
     } else if (warp == 1) {
-        if (lane == 0 && w.rank == 0) run_mma<A_MN, B_MN, PAIR>(p, ring, b, w);
+        if (lane == 0 && w.rank == 0) run_mma<A_MN, B_MN, S>(p, ring, b, w);
     } else {
-        run_epilogue<MODE, PAIR>(maps, p, smem_u32(staging), b, w);
+        run_epilogue<MODE, S>(maps, p, smem_u32(staging), b, w);
     }
 
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (PAIR) {
+    if constexpr (T::PAIRED) {
         tc::cluster_sync();  // the leader's MMAs have drained; the peer's last phases are in peer_last
         if (w.rank == 0 && threadIdx.x == 0) {
 #pragma unroll
-            for (int i = 0; i < STAGES; ++i) {
+            for (int i = 0; i < T::STAGES; ++i) {
                 const int32_t ph = b->peer_last[i];
                 if (ph >= 0 && !mbar_wait_bounded(smem_u32(&b->full[i]), (uint32_t)ph, kWaitLimit))
                     atomicOr(&g_error, 2u);
@@ -710,19 +783,19 @@ __global__ void __launch_bounds__(block_threads(MODE), 1)
     }
     if (warp == 1) {
         tc::fence_after_sync();
-        if constexpr (PAIR)
-            tc::tmem_dealloc_pair(b->tmem_base, TMEM_COLS);
+        if constexpr (T::PAIRED)
+            tc::tmem_dealloc_pair(b->tmem_base, T::TMEM_COLS);
         else
-            tc::tmem_dealloc(b->tmem_base, TMEM_COLS);
+            tc::tmem_dealloc(b->tmem_base, T::TMEM_COLS);
     }
 }
 
 // Adds the pieces of the streamed tiles in the order of K and applies the epilogue.  One tile
 // a blockIdx.y; a warp takes 4 rows x 8 groups of 16 columns, so that slots are read in runs
 // of 128 bytes and rows are written in runs of 256.
-template <int MODE, bool PAIR> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
+template <int MODE, int S> __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
-    constexpr int TM = tile_m<PAIR>(), TN = tile_n<PAIR>(), WIDTH = MODE == UP ? TN / 2 : TN, GROUPS = WIDTH / 16;
+    constexpr int TM = Tile<S>::M, TN = Tile<S>::N, WIDTH = MODE == UP ? TN / 2 : TN, GROUPS = WIDTH / 16;
     griddep_launch();
     griddep_wait();
     const int64_t first = (int64_t)blockIdx.y * p.kblocks, last = first + p.kblocks;  // this tile's K in the range
@@ -793,11 +866,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 }
 
 // Tensor map of an operand in the 128-byte swizzle; what lies outside the tensor reads as zero.  Sets
-// *both where one copy brings both 64-row halves of a 128-row tile:
-//   K contiguous: boxes of 64 K x `rows` rows, 128 or, where the only tile has fewer, as many as it has (rows
+// *both where one copy brings all rows of a CTA:
+//   K contiguous: boxes of 64 K x `rows` rows, those of a CTA or, where the only tile has fewer, as many as it has (rows
 //   of the shared-memory tile that nothing is copied to give accumulator rows that nothing reads);
 //   64 where the halves are apart;
-//   M (N) contiguous: the 64-wide column blocks as a third dimension, boxes of 64 x 64 x 2, where the width
+//   M (N) contiguous: the 64-wide column blocks as a third dimension, boxes of 64 x 64 x rows / 64, where the width
 //   is a multiple of 64, so that no block reaches into the next row.
 bool make_map(CUtensorMap* m, const Mat& t, bool mn, int32_t rows, int32_t* both)
 {
@@ -808,7 +881,7 @@ bool make_map(CUtensorMap* m, const Mat& t, bool mn, int32_t rows, int32_t* both
     const cuuint64_t dims[3] = {(cuuint64_t)(blocks ? ffn::BOX : t.cols), (cuuint64_t)t.rows,
                                 (cuuint64_t)(t.cols / ffn::BOX)};
     const cuuint64_t strides[2] = {(cuuint64_t)t.ld * 2, ffn::BOX * 2};
-    const cuuint32_t box[3] = {ffn::BOX, (cuuint32_t)(mn ? ffn::BOX : rows), 2};
+    const cuuint32_t box[3] = {ffn::BOX, (cuuint32_t)(mn ? ffn::BOX : rows), (cuuint32_t)(rows / ffn::BOX)};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, blocks ? 3 : 2, const_cast<void*>(t.p), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -843,20 +916,20 @@ bool out_maps(ffn::Maps& m, const FfnProduct& g)
 
 // Tile shape of a product and how its last tiles are shared out, from its sizes alone.
 struct Plan {
-    bool pair;
+    int shape;
     int32_t tiles_m, tiles_n, kblocks;
     int64_t tiles, whole;
     int32_t pieces, piece_kb;
 };
 
-// What a shape costs, in microseconds, from runs of both shapes at some twenty sizes (d 64 to
+// What a shape costs, in microseconds, from runs of all shapes at some twenty sizes (d 64 to
 // 5120, width 64 to 13,824, 64 to 30,000 tokens): the launch with its first fill and last drain, a k-block with
-// few workers and with all of them busy (the copies from L2 then bound it), and the least time of
-// a tile (its epilogue).
+// few workers and with all of them busy (the copies from L2 then bound SINGLE and PAIR), the least
+// time of a tile (its epilogue), and what a tile adds to that where the epilogue stands alone.
 struct ShapeCost {
-    double launch, kb_few, kb_busy, tile;
+    double launch, kb_few, kb_busy, tile, alone;
 };
-constexpr ShapeCost kSingle{4.0, 0.25, 0.43, 1.0}, kPair{6.0, 0.31, 0.43, 2.5};
+constexpr ShapeCost kCost[3] = {{4.0, 0.25, 0.43, 1.0, 0.0}, {6.0, 0.31, 0.43, 2.5, 0.0}, {9.0, 0.60, 0.70, 2.5, 4.0}};
 
 // The cheaper way to share out the last tiles of a shape; returns the product's cost.
 double share_out(Plan& r, const ShapeCost& c, int64_t workers, double slot_mb)
@@ -865,7 +938,7 @@ double share_out(Plan& r, const ShapeCost& c, int64_t workers, double slot_mb)
     const int64_t rest = r.tiles % workers, q = rest * r.kblocks;
     r.whole = r.tiles;
     r.pieces = r.piece_kb = 0;
-    double cost = c.launch + (double)(r.tiles / workers) * std::max(r.kblocks * c.kb_busy, c.tile);
+    double cost = c.launch + (double)(r.tiles / workers) * (std::max(r.kblocks * c.kb_busy, c.tile) + c.alone);
     if (!rest) return cost;
     double best = r.kblocks * kb_time(rest) + c.tile;
     const int64_t least = (q + workers - 1) / workers;
@@ -888,17 +961,19 @@ Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 {
     Plan best{};
     double cost = 0;
-    for (int pair = 0; pair < (M > ffn::BM ? 2 : 1); ++pair) {
+    for (int shape = ffn::SINGLE; shape <= ffn::WIDE; ++shape) {
+        if ((shape == ffn::PAIR && M <= 128) || (shape == ffn::WIDE && (M <= 256 || epi == FFN_DACT))) continue;
         Plan r{};
-        r.pair = pair;
-        const int64_t tm = pair ? 256 : 128, tn = epi == FFN_UP ? tm / 2 : tm;
+        r.shape = shape;
+        const int64_t tm = shape == ffn::SINGLE ? 128 : shape == ffn::PAIR ? 256 : 512;
+        const int64_t tw = shape == ffn::SINGLE ? 128 : 256, tn = epi == FFN_UP ? tw / 2 : tw;
         r.kblocks = (int32_t)((K + ffn::BK - 1) / ffn::BK);
         r.tiles_m = (int32_t)((M + tm - 1) / tm);
         r.tiles_n = (int32_t)((N + tn - 1) / tn);
         r.tiles = (int64_t)r.tiles_m * r.tiles_n;
-        const double slot_mb = (double)std::min(M, tm) * (double)tm * 4e-6;
-        const double c = share_out(r, pair ? kPair : kSingle, pair ? ffn::B200_SMS / 2 : ffn::B200_SMS, slot_mb);
-        if (!pair || c < cost) {
+        const double slot_mb = (double)std::min(M, tm) * (double)tw * 4e-6;
+        const double c = share_out(r, kCost[shape], shape == ffn::SINGLE ? ffn::B200_SMS : ffn::B200_SMS / 2, slot_mb);
+        if (!cost || c < cost) {
             best = r;
             cost = c;
         }
@@ -906,10 +981,11 @@ Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
     return best;
 }
 
-template <int MODE, bool A_MN, bool B_MN, bool PAIR>
+template <int MODE, bool A_MN, bool B_MN, int S>
 cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
 {
-    auto kern = ffn::k_product<MODE, A_MN, B_MN, PAIR>;
+    auto kern = ffn::k_product<MODE, A_MN, B_MN, S>;
+    constexpr bool PAIRED = ffn::Tile<S>::PAIRED;
     constexpr int kMaxDevices = 64;
     static int workers_dev[kMaxDevices] = {};  // resident CTAs or pairs, once the attribute is set
     static std::mutex mu;
@@ -925,19 +1001,19 @@ cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool afte
     la[1].val.clusterDim.y = 1;
     la[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(ffn::block_threads(MODE));
-    cfg.dynamicSmemBytes = ffn::kSmemBytes;
+    cfg.blockDim = dim3(ffn::block_threads(MODE, S));
+    cfg.dynamicSmemBytes = ffn::smem_bytes<S>();
     cfg.stream = s;
     cfg.attrs = after ? la : la + 1;
-    cfg.numAttrs = (after ? 1 : 0) + (PAIR ? 1 : 0);
+    cfg.numAttrs = (after ? 1 : 0) + (PAIRED ? 1 : 0);
     int64_t workers;
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!workers_dev[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn::kSmemBytes);
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn::smem_bytes<S>());
             if (e != cudaSuccess) return e;
             int n = sm_count();
-            if (PAIR) {
+            if (PAIRED) {
                 cudaLaunchConfig_t q = cfg;
                 q.attrs = la + 1;
                 q.numAttrs = 1;
@@ -949,23 +1025,24 @@ cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool afte
         workers = workers_dev[dev];
     }
     workers = std::min<int64_t>(std::max<int64_t>(p.whole, p.pieces), workers);
-    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * workers : workers));
+    cfg.gridDim = dim3((unsigned)(PAIRED ? 2 * workers : workers));
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
 template <int MODE, bool A_MN, bool B_MN>
-cudaError_t launch_shape(bool pair, const ffn::Maps& maps, const ffn::Params& p, bool after,
-                         cudaStream_t s)
+cudaError_t launch_shape(int shape, const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
 {
-    return pair ? launch_kernel<MODE, A_MN, B_MN, true>(maps, p, after, s)
-                : launch_kernel<MODE, A_MN, B_MN, false>(maps, p, after, s);
+    if (shape == ffn::SINGLE) return launch_kernel<MODE, A_MN, B_MN, ffn::SINGLE>(maps, p, after, s);
+    if (shape == ffn::PAIR) return launch_kernel<MODE, A_MN, B_MN, ffn::PAIR>(maps, p, after, s);
+    if constexpr (MODE != ffn::DACT) return launch_kernel<MODE, A_MN, B_MN, ffn::WIDE>(maps, p, after, s);
+    return cudaErrorInvalidValue;
 }
 
-template <int MODE, bool PAIR> cudaError_t launch_join(const ffn::Params& p, cudaStream_t s)
+template <int MODE, int S> cudaError_t launch_join(const ffn::Params& p, cudaStream_t s)
 {
     // a warp takes 4 rows x up to 128 columns of one tile
-    const int64_t warps = (std::min<int64_t>(p.M, ffn::tile_m<PAIR>()) + 3) / 4 *
-                          std::max(1, ffn::tile_n<PAIR>() / (MODE == ffn::UP ? 256 : 128));
+    const int64_t warps = (std::min<int64_t>(p.M, ffn::Tile<S>::M) + 3) / 4 *
+                          std::max(1, ffn::Tile<S>::N / (MODE == ffn::UP ? 256 : 128));
     cudaLaunchAttribute la[1];
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     la[0].val.programmaticStreamSerializationAllowed = 1;
@@ -975,12 +1052,14 @@ template <int MODE, bool PAIR> cudaError_t launch_join(const ffn::Params& p, cud
     cfg.stream = s;
     cfg.attrs = la;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ffn::k_join<MODE, PAIR>, p);
+    return cudaLaunchKernelEx(&cfg, ffn::k_join<MODE, S>, p);
 }
 
-template <int MODE> cudaError_t launch_join(bool pair, const ffn::Params& p, cudaStream_t s)
+template <int MODE> cudaError_t launch_join(int shape, const ffn::Params& p, cudaStream_t s)
 {
-    return pair ? launch_join<MODE, true>(p, s) : launch_join<MODE, false>(p, s);
+    return shape == ffn::SINGLE ? launch_join<MODE, ffn::SINGLE>(p, s)
+           : shape == ffn::PAIR ? launch_join<MODE, ffn::PAIR>(p, s)
+                                : launch_join<MODE, ffn::WIDE>(p, s);
 }
 
 bool on32(const void* p, int64_t ld, int64_t esz) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld * esz % 32 == 0; }
@@ -990,7 +1069,7 @@ bool on32(const void* p, int64_t ld, int64_t esz) { return (reinterpret_cast<uin
 size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K)
 {
     const Plan r = plan(epi, M, N, K);
-    return (size_t)r.pieces * 2 * (r.pair ? 256 * 256 : 128 * 128) * 4;
+    return (size_t)r.pieces * 2 * (r.shape == ffn::SINGLE ? 128 * 128 : r.shape == ffn::PAIR ? 256 * 256 : 512 * 256) * 4;
 }
 
 cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
@@ -998,11 +1077,16 @@ cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
     ffn::Maps maps;
     const Plan r = plan(g.epi, g.M, g.N, g.K);
     ffn::Params p{};
-    int32_t a_rows = !r.pair && !g.a_mn && r.tiles_m == 1 ? (int32_t)((g.M + 7) / 8 * 8) : ffn::BM;
+    if (r.tiles >= (int64_t)1 << 31) {
+        record_error("the product has more than 2^31 tiles");
+        return cudaErrorInvalidValue;
+    }
+    int32_t a_rows = r.shape == ffn::WIDE ? 2 * ffn::BM : ffn::BM;
+    if (r.shape == ffn::SINGLE && !g.a_mn && r.tiles_m == 1) a_rows = (int32_t)((g.M + 7) / 8 * 8);
     if (a_rows == ffn::BOX) a_rows += 8;  // 64 means two boxes
-    p.stage_bytes = ffn::OP_BYTES + a_rows * ffn::BK * 2;
+    p.stage_bytes = a_rows * ffn::BK * 2 + ffn::BM * ffn::BK * 2;
     if (!make_map(&maps.a, g.a, g.a_mn, a_rows, &p.a_blocks) ||
-        !make_map(&maps.b, g.b, g.b_mn, g.epi == FFN_UP && !r.pair ? ffn::BOX : ffn::BM, &p.b_blocks) ||
+        !make_map(&maps.b, g.b, g.b_mn, g.epi == FFN_UP && r.shape == ffn::SINGLE ? ffn::BOX : ffn::BM, &p.b_blocks) ||
         !out_maps(maps, g)) {
         record_error("tensor map encoding failed (cuTensorMapEncodeTiled unavailable or refused the layout)");
         return cudaErrorInvalidValue;
@@ -1029,19 +1113,19 @@ cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
              (g.epi == FFN_STORE || g.N % 16 == 0);
     cudaError_t e;
     if (g.epi == FFN_UP)
-        e = launch_shape<ffn::UP, false, false>(r.pair, maps, p, after, s);
+        e = launch_shape<ffn::UP, false, false>(r.shape, maps, p, after, s);
     else if (g.epi == FFN_DACT)
-        e = launch_shape<ffn::DACT, false, true>(r.pair, maps, p, after, s);
+        e = launch_shape<ffn::DACT, false, true>(r.shape, maps, p, after, s);
     else if (g.a_mn)  // dW: both operands with M, N contiguous
-        e = launch_shape<ffn::STORE, true, true>(r.pair, maps, p, after, s);
+        e = launch_shape<ffn::STORE, true, true>(r.shape, maps, p, after, s);
     else if (g.b_mn)  // dx
-        e = launch_shape<ffn::STORE, false, true>(r.pair, maps, p, after, s);
+        e = launch_shape<ffn::STORE, false, true>(r.shape, maps, p, after, s);
     else  // y
-        e = launch_shape<ffn::STORE, false, false>(r.pair, maps, p, after, s);
+        e = launch_shape<ffn::STORE, false, false>(r.shape, maps, p, after, s);
     if (e != cudaSuccess || !r.pieces) return e;
-    if (g.epi == FFN_UP) return launch_join<ffn::UP>(r.pair, p, s);
-    if (g.epi == FFN_DACT) return launch_join<ffn::DACT>(r.pair, p, s);
-    return launch_join<ffn::STORE>(r.pair, p, s);
+    if (g.epi == FFN_UP) return launch_join<ffn::UP>(r.shape, p, s);
+    if (g.epi == FFN_DACT) return launch_join<ffn::DACT>(r.shape, p, s);
+    return launch_join<ffn::STORE>(r.shape, p, s);
 }
 
 uint32_t ffn_device_error(bool clear)
