@@ -6,7 +6,8 @@
 //                dx = du . W_up,  dW_up = du^T . x,  dW_down = dy^T . act
 //
 // One kernel for all: C[M, N] = A . B^T over K, each operand stored with K contiguous or
-// with M (N) contiguous.  A stage of the shared-memory ring holds 128 x 64 of A and
+// with M (N) contiguous; the last three run in one launch, which fills the GPU where each alone would
+// leave a part of it idle.  A stage of the shared-memory ring holds 128 x 64 of A and
 // 128 x 64 of B as four 64 x 64 boxes of 8 KiB that the tensor copy writes in the 128-byte
 // swizzle; a box has the contiguous dimension of its operand along its rows, so both
 // layouts cost the same copies and differ only in the matrix descriptor (smem_desc_mn) and
@@ -101,17 +102,27 @@ static_assert(smem_bytes<WIDE>() <= 232448 && smem_bytes<PAIR>() <= 232448, "sha
 
 __device__ uint32_t g_error;
 
-struct Params {
+constexpr int MAX_PRODUCTS = 3;
+
+// One product of a launch.  Its tiles [0, whole) are worked on whole, one after another by each
+// worker; tiles [whole, tiles) are the rest, which all products of the launch share out together.
+struct Product {
     int32_t M, N, kblocks;       // N: columns of the output (UP: inner)
     int32_t tiles_m, tiles_n;
-    int64_t whole, tiles;        // tiles [0, whole) are worked on whole, one after another by each worker
-    int32_t pieces, piece_kb;    // tiles [whole, tiles): their K end to end in `pieces` of piece_kb blocks
+    int64_t whole, tiles;
+    int32_t a_mn;                // STORE: A is stored with M contiguous
     int32_t stage_bytes;         // bytes that the copies of one CTA and stage bring
     int32_t a_blocks, b_blocks;  // 1: one copy brings a CTA's rows of the operand (see make_map)
     int32_t out_f32, accumulate;
     int32_t wide;                // rows of out, u and du (and their second halves) begin on 32-byte boundaries
     void* out;
     int64_t ld_out;
+};
+struct Params {
+    Product g[MAX_PRODUCTS];
+    int32_t n;                   // products
+    int32_t pieces, piece_kb;    // the rest's K end to end in `pieces` of piece_kb blocks; 0: whole tiles
+    int64_t rest_tiles, rest_kb;
     bf16* u;
     int64_t ld_u;
     bf16* du;
@@ -132,18 +143,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr)
 // Tensor maps of one launch: the operands, and what the epilogue copies through shared memory
 // (STORE: out; UP and DACT: act, the halves of u, the halves of du; boxes as in out_map).
 struct Maps {
-    CUtensorMap a, b, out, u_a, u_b, du_a, du_b;
+    CUtensorMap a[MAX_PRODUCTS], b[MAX_PRODUCTS], out[MAX_PRODUCTS], u_a, u_b, du_a, du_b;
 };
 
-// A piece of work: K blocks [kb0, kb1) of a tile; slot >= 0 where they are not all of its K.
+// A piece of work: K blocks [kb0, kb1) of a tile of product g; slot >= 0 where they are not all
+// of its K.
 struct Piece {
-    int32_t m_blk, n_blk, kb0, kb1;
+    int32_t g, m_blk, n_blk, kb0, kb1;
     int64_t slot;
 };
 
 // Tile t -> its blocks of rows and columns, in groups of GROUP_M m-blocks so that the tiles
 // worked on at one time share rows of A and of B in L2.
-__device__ __forceinline__ void tile_at(int64_t t, const Params& p, int32_t& m_blk, int32_t& n_blk)
+__device__ __forceinline__ void tile_at(int64_t t, const Product& p, int32_t& m_blk, int32_t& n_blk)
 {
     const uint32_t per_group = GROUP_M * (uint32_t)p.tiles_n, g = (uint32_t)t / per_group;  // tiles: below 2^31
     const uint32_t gm = min((uint32_t)GROUP_M, (uint32_t)p.tiles_m - g * GROUP_M);
@@ -152,37 +164,64 @@ __device__ __forceinline__ void tile_at(int64_t t, const Params& p, int32_t& m_b
     n_blk = (int32_t)(local / gm);
 }
 
-// The pieces of one worker, the same sequence for every role: whole tiles, then its share of
-// the streamed K range.  A share begins inside a tile (slot 0 of the worker) at most once and
-// ends inside another (slot 1) at most once.
+// The pieces of one worker, the same sequence for every role: its whole tiles of each product, then
+// its part of the rest: whole tiles, or a share of their K end to end.  A share begins inside a
+// tile (slot 0 of the share) at most once and ends inside another (slot 1) at most once.
 struct Walk {
-    int64_t t, q, end, worker;
+    int32_t g;
+    int64_t t, q, end, share, worker;
 };
 
-__device__ __forceinline__ Walk walk_begin(int64_t worker) { return Walk{worker, 0, 0, worker}; }
+__device__ __forceinline__ Walk walk_begin(int64_t worker) { return Walk{0, worker, 0, 0, worker, worker}; }
 
 __device__ __forceinline__ bool walk_next(Walk& w, const Params& p, int64_t n_workers, Piece& x)
 {
-    if (w.t < p.whole) {
-        tile_at(w.t, p, x.m_blk, x.n_blk);
+    for (; w.g < p.n; ++w.g, w.t = w.worker) {
+        const Product& c = p.g[w.g];
+        if (w.t < c.whole) {
+            x.g = w.g;
+            x.kb0 = 0;
+            x.kb1 = c.kblocks;
+            x.slot = -1;
+            tile_at(w.t, c, x.m_blk, x.n_blk);
+            w.t += n_workers;
+            return true;
+        }
+    }
+    if (!p.pieces) {
+        int64_t r = w.share;
+        if (r >= p.rest_tiles) return false;
+        w.share += n_workers;
+        int32_t g = 0;
+        for (; r >= p.g[g].tiles - p.g[g].whole; ++g) r -= p.g[g].tiles - p.g[g].whole;
+        x.g = g;
         x.kb0 = 0;
-        x.kb1 = p.kblocks;
+        x.kb1 = p.g[g].kblocks;
         x.slot = -1;
-        w.t += n_workers;
+        tile_at(p.g[g].whole + r, p.g[g], x.m_blk, x.n_blk);
         return true;
     }
     if (w.q >= w.end) {
-        if (w.worker >= p.pieces) return false;
-        w.q = w.worker * p.piece_kb;
-        w.end = min(w.q + p.piece_kb, (p.tiles - p.whole) * p.kblocks);
-        w.t = p.whole + w.worker;  // from here on: the share's number
-        w.worker += n_workers;
+        if (w.share >= p.pieces) return false;
+        w.q = w.share * p.piece_kb;
+        w.end = min(w.q + p.piece_kb, p.rest_kb);
+        w.t = w.share;  // from here on: the share at work
+        w.share += n_workers;
     }
-    const int64_t tile = w.q / p.kblocks;
-    x.kb0 = (int32_t)(w.q - tile * p.kblocks);
-    x.kb1 = (int32_t)min((int64_t)p.kblocks, x.kb0 + (w.end - w.q));
-    tile_at(p.whole + tile, p, x.m_blk, x.n_blk);
-    x.slot = x.kb0 == 0 && x.kb1 == p.kblocks ? -1 : 2 * (w.t - p.whole) + (x.kb0 == 0 ? 1 : 0);
+    int64_t q = w.q;
+    int32_t g = 0;
+    for (;; ++g) {
+        const int64_t kb = (p.g[g].tiles - p.g[g].whole) * p.g[g].kblocks;
+        if (q < kb) break;
+        q -= kb;
+    }
+    const Product& c = p.g[g];
+    const int64_t tile = q / c.kblocks;
+    x.g = g;
+    x.kb0 = (int32_t)(q - tile * c.kblocks);
+    x.kb1 = (int32_t)min((int64_t)c.kblocks, x.kb0 + (w.end - w.q));
+    tile_at(c.whole + tile, c, x.m_blk, x.n_blk);
+    x.slot = x.kb0 == 0 && x.kb1 == c.kblocks ? -1 : 2 * w.t + (x.kb0 == 0 ? 1 : 0);
     w.q += x.kb1 - x.kb0;
     return true;
 }
@@ -213,17 +252,17 @@ __device__ __forceinline__ void raise_abort(Bars* b, uint32_t code)
 
 // A CTA's rows of one operand, BOXES times 64 of them ([x0, x0 + 64), [x1, x1 + 64), then on from x0 + 128),
 // for the 64 K from k on: one copy where the map's box holds them all, else one for each 64.
-template <bool MN, int BOXES>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int32_t form, int32_t x0, int32_t x1,
-                                             int32_t k, uint32_t bar, bool remote)
+template <int BOXES>
+__device__ __forceinline__ void load_operand(bool mn, uint32_t dst, const CUtensorMap* map, int32_t form, int32_t x0,
+                                             int32_t x1, int32_t k, uint32_t bar, bool remote)
 {
-    if (MN && form) {
+    if (mn && form) {
         remote ? tc::tma_load_3d_pair(dst, map, 0, k, x0 / BOX, bar) : tc::tma_load_3d(dst, map, 0, k, x0 / BOX, bar);
         return;
     }
 #pragma unroll
     for (int i = 0; i < BOXES; ++i) {
-        const int32_t x = i == 1 ? x1 : x0 + i * BOX, c = MN ? x : k, r = MN ? k : x;
+        const int32_t x = i == 1 ? x1 : x0 + i * BOX, c = mn ? x : k, r = mn ? k : x;
         remote ? tc::tma_load_2d_pair(dst + i * BOX_BYTES, map, c, r, bar) : tc::tma_load_2d(dst + i * BOX_BYTES, map, c, r, bar);
         if (form) return;
     }
@@ -233,9 +272,8 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 // gated half and 64 of the other for UP in the single shape; in a pair the leader loads the
 // gated half, the peer the other).  The peer's copies complete on the leader's barrier,
 // which the leader armed for both CTAs' bytes.
-template <int MODE, bool A_MN, bool B_MN, int S>
-__device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, const Params& p, uint8_t* ring, Bars* b,
-                             const Where& w)
+template <int MODE, bool B_MN, int S>
+__device__ void run_producer(const Maps& maps, const Params& p, uint8_t* ring, Bars* b, const Where& w)
 {
     using T = Tile<S>;
     constexpr int STAGES = T::STAGES;
@@ -248,15 +286,18 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
     Walk walk = walk_begin(w.worker);
     Piece it;
     while (!b->abort && walk_next(walk, p, w.n_workers, it)) {
+        const Product& c = p.g[it.g];
+        const CUtensorMap *tmA = &maps.a[it.g], *tmB = &maps.b[it.g];
+        const bool a_mn = MODE == STORE && B_MN && c.a_mn;
         const int32_t ma = it.m_blk * T::M + (int32_t)w.rank * T::ROWS;
         int32_t n0, n1;
         if (MODE == UP) {
             if (T::PAIRED) {
-                n0 = it.n_blk * 128 + (w.rank ? p.N : 0);
+                n0 = it.n_blk * 128 + (w.rank ? c.N : 0);
                 n1 = n0 + BOX;
             } else {
                 n0 = it.n_blk * 64;
-                n1 = p.N + n0;
+                n1 = c.N + n0;
             }
         } else {
             n0 = it.n_blk * T::N + (int32_t)w.rank * 128;
@@ -272,9 +313,9 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
             if (remote)
                 bar = tc::mapa(bar, 0);
             else
-                mbar_arrive_expect_tx(bar, T::PAIRED ? 2 * p.stage_bytes : p.stage_bytes);
-            load_operand<A_MN, T::ROWS / BOX>(dst, tmA, p.a_blocks, ma, ma + BOX, kb * BK, bar, remote);
-            load_operand<B_MN, 2>(dst + T::A_BYTES, tmB, p.b_blocks, n0, n1, kb * BK, bar, remote);
+                mbar_arrive_expect_tx(bar, T::PAIRED ? 2 * c.stage_bytes : c.stage_bytes);
+            load_operand<T::ROWS / BOX>(a_mn, dst, tmA, c.a_blocks, ma, ma + BOX, kb * BK, bar, remote);
+            load_operand<2>(B_MN, dst + T::A_BYTES, tmB, c.b_blocks, n0, n1, kb * BK, bar, remote);
             last[s] = (int32_t)phase;
             if (++s == STAGES) {
                 s = 0;
@@ -296,14 +337,13 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
 }
 
 // MMA issuer (one thread; the leader's in a pair).
-template <bool A_MN, bool B_MN, int S>
+template <int MODE, bool B_MN, int S>
 __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
 {
     using T = Tile<S>;
-    const uint32_t idesc = tc::idesc_bf16_f32(T::PAIRED ? 2 * BM : BM, T::N) | (A_MN ? 1u << 15 : 0u) |
-                           (B_MN ? 1u << 16 : 0u);
+    const uint32_t idesc0 = tc::idesc_bf16_f32(T::PAIRED ? 2 * BM : BM, T::N) | (B_MN ? 1u << 16 : 0u);
     // UK elements of K further: 32 bytes inside a swizzled row, or two 8-row atoms
-    constexpr uint64_t A_STEP = A_MN ? 2048 >> 4 : 32 >> 4, B_STEP = B_MN ? 2048 >> 4 : 32 >> 4;
+    constexpr uint64_t B_STEP = B_MN ? 2048 >> 4 : 32 >> 4;
     constexpr uint64_t A_HALF = BM * BK * 2 >> 4;
     int s = 0;
     uint32_t phase = 0;
@@ -313,6 +353,9 @@ __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
     bool more = walk_next(walk, p, w.n_workers, next);
     for (; more && !b->abort; ++n) {
         const Piece it = next;
+        const bool a_mn = MODE == STORE && B_MN && p.g[it.g].a_mn;
+        const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u);
+        const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4;
         const int ab = T::ACCS == 2 ? (int)(n & 1) : 0;
         const uint32_t acc_phase = (uint32_t)(T::ACCS == 2 ? n >> 1 : n) & 1u;
         if (!wait_or_abort<T::PAIRED>(smem_u32(&b->acc_empty[ab]), acc_phase ^ 1u, b)) {
@@ -330,7 +373,7 @@ __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
             }
             tc::fence_after_sync();
             const uint32_t a_addr = smem_u32(ring + (size_t)s * T::STAGE_BYTES), b_addr = a_addr + T::A_BYTES;
-            const uint64_t a_desc = A_MN ? smem_desc_mn(a_addr) : tc::smem_desc_sw128(a_addr);
+            const uint64_t a_desc = a_mn ? smem_desc_mn(a_addr) : tc::smem_desc_sw128(a_addr);
             const uint64_t b_desc = B_MN ? smem_desc_mn(b_addr) : tc::smem_desc_sw128(b_addr);
 #pragma unroll
             for (int kk = 0; kk < BK / UK; ++kk) {
@@ -338,9 +381,9 @@ __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
 #pragma unroll
                 for (int h = 0; h < T::HALVES; ++h) {
                     if (T::PAIRED)
-                        tc::mma_bf16_pair(d + h * T::N, a_desc + h * A_HALF + kk * A_STEP, b_desc + kk * B_STEP, idesc, acc);
+                        tc::mma_bf16_pair(d + h * T::N, a_desc + h * A_HALF + kk * a_step, b_desc + kk * B_STEP, idesc, acc);
                     else
-                        tc::mma_bf16(d, a_desc + kk * A_STEP, b_desc + kk * B_STEP, idesc, acc);
+                        tc::mma_bf16(d, a_desc + kk * a_step, b_desc + kk * B_STEP, idesc, acc);
                 }
             }
             const uint32_t e = smem_u32(&b->empty[s]);
@@ -434,13 +477,13 @@ __device__ __forceinline__ void get16(const bf16* src, uint4& lo, uint4& hi, int
 // The epilogue of 16 columns of one row, the first n of them inside the output.  STORE: v is
 // the product.  UP: v and g are a and b.  DACT: v is d_act, ua and ub hold a and b.
 template <int MODE>
-__device__ __forceinline__ void finish16(const Params& p, int64_t row, int32_t col, int n, float* v, const float* g,
+__device__ __forceinline__ void finish16(const Params& q, const Product& p, int64_t row, int32_t col, int n, float* v, const float* g,
                                          const uint4* ua, const uint4* ub)
 {
     if constexpr (MODE == UP) {
-        if (p.u) {
-            put16(p.u + row * p.ld_u + col, v, n, p.wide);
-            put16(p.u + row * p.ld_u + p.N + col, g, n, p.wide);
+        if (q.u) {
+            put16(q.u + row * q.ld_u + col, v, n, p.wide);
+            put16(q.u + row * q.ld_u + p.N + col, g, n, p.wide);
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = v[e] * sigmoid_fast(v[e]) * g[e];
@@ -453,21 +496,21 @@ __device__ __forceinline__ void finish16(const Params& p, int64_t row, int32_t c
         unpack<bf16>(ub[1], b + 8);
 #pragma unroll
         for (int e = 0; e < 16; ++e) dact_one(v[e], a[e], b[e]);
-        put16(p.du + row * p.ld_du + col, a, n, p.wide);
-        put16(p.du + row * p.ld_du + p.N + col, b, n, p.wide);
+        put16(q.du + row * q.ld_du + col, a, n, p.wide);
+        put16(q.du + row * q.ld_du + p.N + col, b, n, p.wide);
         if (p.out) put16(static_cast<bf16*>(p.out) + row * p.ld_out + col, v, n, p.wide);
     } else if (p.out_f32) {
         float* dst = static_cast<float*>(p.out) + row * p.ld_out + col;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             if (4 * h >= n) break;
-            float4* q = reinterpret_cast<float4*>(dst + 4 * h);
+            float4* at = reinterpret_cast<float4*>(dst + 4 * h);
             float4 x = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
             if (p.accumulate) {
-                const float4 o = *q;
+                const float4 o = *at;
                 x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
             }
-            *q = x;
+            *at = x;
         }
     } else {
         bf16* dst = static_cast<bf16*>(p.out) + row * p.ld_out + col;
@@ -531,6 +574,8 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
     Walk walk = walk_begin(w.worker);
     Piece it;
     for (; ok && walk_next(walk, p, w.n_workers, it); ++n) {
+        const Product& c0 = p.g[it.g];
+        const int32_t M = c0.M, N = c0.N;
         const int ab = T::ACCS == 2 ? (int)(n & 1) : 0;
         const uint32_t acc_phase = (uint32_t)(T::ACCS == 2 ? n >> 1 : n) & 1u;
         const int32_t row0 = it.m_blk * TM + (int32_t)w.rank * T::ROWS + half * BM + quarter * 32;  // of this warp
@@ -545,7 +590,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
             }
             u_pending = true;
         };
-        if (MODE == DACT && whole && row0 < p.M && col0 < p.N) fetch_u(col0);
+        if (MODE == DACT && whole && row0 < M && col0 < N) fetch_u(col0);
         const bool got = wait_or_abort<T::PAIRED>(smem_u32(&b->acc_full[ab]), acc_phase, b);
         if (!__all_sync(0xffffffffu, got)) {
             raise_abort(b, 32u);
@@ -559,10 +604,10 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
             const int32_t col = col0 + 32 * c;
             tc::ld32(t + 32 * c, v);
             if constexpr (MODE == UP) tc::ld32(t + WIDTH + 32 * c, g);
-            if (row0 >= p.M || col >= p.N) continue;
+            if (row0 >= M || col >= N) continue;
             if (!whole) {
                 // [column group of 8][row][8]: a warp's 32 rows are 1 KiB in a row
-                if (row0 + lane >= p.M) continue;
+                if (row0 + lane >= M) continue;
                 float* q = p.slots + ((it.slot * (TN / 8) + 4 * (part * CH + c)) * TM + (row0 - it.m_blk * TM) + lane) * 8;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -576,11 +621,11 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                 continue;
             }
             if constexpr (MODE == STORE) {
-                if (p.out_f32 || p.accumulate) {
-                    const int n0 = inside(col, p.N), n1 = inside(col + 16, p.N);
-                    if (row0 + lane < p.M) {
-                        if (n0) finish16<MODE>(p, row0 + lane, col, n0, v, g, nullptr, nullptr);
-                        if (n1) finish16<MODE>(p, row0 + lane, col + 16, n1, v + 16, g, nullptr, nullptr);
+                if (c0.out_f32 || c0.accumulate) {
+                    const int n0 = inside(col, N), n1 = inside(col + 16, N);
+                    if (row0 + lane < M) {
+                        if (n0) finish16<MODE>(p, c0, row0 + lane, col, n0, v, g, nullptr, nullptr);
+                        if (n1) finish16<MODE>(p, c0, row0 + lane, col + 16, n1, v + 16, g, nullptr, nullptr);
                     }
                     continue;
                 }
@@ -593,11 +638,11 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sts16(cell128(dst, lane, 4 * (c & 1) + j), pack<bf16>(v + 8 * j));
-                if ((c & 1) || col + 32 >= p.N) {
+                if ((c & 1) || col + 32 >= N) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tc::tma_store_2d(&maps.out, dst, col - 32 * (c & 1), row0);
+                        tc::tma_store_2d(&maps.out[it.g], dst, col - 32 * (c & 1), row0);
                         tc::bulk_commit();
                     }
                 }
@@ -634,7 +679,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tc::tma_store_2d(&maps.out, dst, col, row0);
+                    tc::tma_store_2d(&maps.out[it.g], dst, col, row0);
                     tc::bulk_commit();
                 }
             } else if constexpr (MODE == UP) {
@@ -658,7 +703,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                         tc::tma_store_2d(&maps.u_a, box, col, row0);
                         tc::tma_store_2d(&maps.u_b, box + BOX32, col, row0);
                     }
-                    tc::tma_store_2d(&maps.out, box + 2 * BOX32, col, row0);
+                    tc::tma_store_2d(&maps.out[it.g], box + 2 * BOX32, col, row0);
                     tc::bulk_commit();
                 }
             } else {
@@ -686,10 +731,10 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                 if (lane == 0) {
                     tc::tma_store_2d(&maps.du_a, box, col, row0);
                     tc::tma_store_2d(&maps.du_b, box + BOX32, col, row0);
-                    if (p.out) tc::tma_store_2d(&maps.out, box + 2 * BOX32, col, row0);
+                    if (c0.out) tc::tma_store_2d(&maps.out[it.g], box + 2 * BOX32, col, row0);
                     tc::bulk_commit();
                 }
-                if (c + 1 < CH && col + 32 < p.N) fetch_u(col + 32);
+                if (c + 1 < CH && col + 32 < N) fetch_u(col + 32);
             }
         }
         tc::fence_before_sync();
@@ -708,7 +753,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
     __syncwarp();
 }
 
-template <int MODE, bool A_MN, bool B_MN, int S>
+template <int MODE, bool B_MN, int S>
 __global__ void __launch_bounds__(block_threads(MODE, S), 1)
     k_product(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 {
@@ -740,8 +785,10 @@ __global__ void __launch_bounds__(block_threads(MODE, S), 1)
         mbar_init(smem_u32(&b->drain), 1);
         b->abort = 0;
         mbar_fence_init();
-        tc::prefetch_tmap(&maps.a);
-        tc::prefetch_tmap(&maps.b);
+        for (int i = 0; i < p.n; ++i) {
+            tc::prefetch_tmap(&maps.a[i]);
+            tc::prefetch_tmap(&maps.b[i]);
+        }
     }
     if (warp == 1) {
         if constexpr (T::PAIRED) {
@@ -760,9 +807,9 @@ __global__ void __launch_bounds__(block_threads(MODE, S), 1)
     griddep_launch();
     griddep_wait();
     if (warp == 0) {
-        if (lane == 0) run_producer<MODE, A_MN, B_MN, S>(&maps.a, &maps.b, p, ring, b, w);
+        if (lane == 0) run_producer<MODE, B_MN, S>(maps, p, ring, b, w);
     } else if (warp == 1) {
-        if (lane == 0 && w.rank == 0) run_mma<A_MN, B_MN, S>(p, ring, b, w);
+        if (lane == 0 && w.rank == 0) run_mma<MODE, B_MN, S>(p, ring, b, w);
     } else {
         run_epilogue<MODE, S>(maps, p, smem_u32(staging), b, w);
     }
@@ -798,12 +845,20 @@ template <int MODE, int S> __global__ void __launch_bounds__(256) k_join(const _
     constexpr int TM = Tile<S>::M, TN = Tile<S>::N, WIDTH = MODE == UP ? TN / 2 : TN, GROUPS = WIDTH / 16;
     griddep_launch();
     griddep_wait();
-    const int64_t first = (int64_t)blockIdx.y * p.kblocks, last = first + p.kblocks;  // this tile's K in the range
-    const int64_t w0 = first / p.piece_kb, w1 = (last - 1) / p.piece_kb;
+    int64_t tile = blockIdx.y, first = 0;  // this tile's K among the rest's
+    int g = 0;
+    for (; tile >= p.g[g].tiles - p.g[g].whole; ++g) {
+        const int64_t n = p.g[g].tiles - p.g[g].whole;
+        tile -= n;
+        first += n * p.g[g].kblocks;
+    }
+    const Product& c0 = p.g[g];
+    first += tile * c0.kblocks;
+    const int64_t w0 = first / p.piece_kb, w1 = (first + c0.kblocks - 1) / p.piece_kb;
     if (w0 == w1) return;  // the whole tile was one worker's
     int32_t m_blk, n_blk;
-    tile_at(p.whole + blockIdx.y, p, m_blk, n_blk);
-    const int rows = (int)min((int64_t)TM, (int64_t)p.M - (int64_t)m_blk * TM);
+    tile_at(c0.whole + tile, c0, m_blk, n_blk);
+    const int rows = (int)min((int64_t)TM, (int64_t)c0.M - (int64_t)m_blk * TM);
     const int lane = threadIdx.x & 31;
     constexpr int ACROSS = GROUPS < 8 ? GROUPS : 8, STEPS = GROUPS / ACROSS;
     for (int i = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < (rows + 3) / 4 * STEPS;
@@ -812,7 +867,7 @@ template <int MODE, int S> __global__ void __launch_bounds__(256) k_join(const _
         const int r = (i / STEPS) * 4 + (lane & 3), c = (i % STEPS) * ACROSS + (lane >> 2);
         const int64_t row = (int64_t)m_blk * TM + r;
         const int32_t col = n_blk * WIDTH + 16 * c;
-        const int n = inside(col, p.N);
+        const int n = inside(col, c0.N);
         if (r >= rows || n == 0) continue;
         float v[16] = {}, g[16] = {};
 #pragma unroll 2
@@ -837,10 +892,10 @@ template <int MODE, int S> __global__ void __launch_bounds__(256) k_join(const _
         }
         uint4 ua[2], ub[2];
         if constexpr (MODE == DACT) {
-            get16(p.u + row * p.ld_u + col, ua[0], ua[1], n, p.wide);
-            get16(p.u + row * p.ld_u + p.N + col, ub[0], ub[1], n, p.wide);
+            get16(p.u + row * p.ld_u + col, ua[0], ua[1], n, c0.wide);
+            get16(p.u + row * p.ld_u + c0.N + col, ub[0], ub[1], n, c0.wide);
         }
-        finish16<MODE>(p, row, col, n, v, g, ua, ub);
+        finish16<MODE>(p, c0, row, col, n, v, g, ua, ub);
     }
 }
 
@@ -903,23 +958,26 @@ bool out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t width, int64_t
 }
 
 // The maps of a product's epilogue; a single row's stride counts as its width.
-bool out_maps(ffn::Maps& m, const FfnProduct& g)
+bool out_maps(ffn::Maps& m, int i, const FfnProduct& g)
 {
     auto one = [&](CUtensorMap* t, const void* p, int64_t ld, int32_t cols) {
         return !p || out_map(t, p, g.M, g.N, ld, cols);
     };
     const bf16 *u = static_cast<const bf16*>(g.u), *du = static_cast<const bf16*>(g.du);
-    if (g.epi == FFN_STORE) return g.out_f32 || g.accumulate || one(&m.out, g.out, g.ld_out, 64);
-    return one(&m.out, g.out, g.ld_out, 32) && one(&m.u_a, u, g.ld_u, 32) && one(&m.u_b, u ? u + g.N : u, g.ld_u, 32) &&
+    if (g.epi == FFN_STORE) return g.out_f32 || g.accumulate || one(&m.out[i], g.out, g.ld_out, 64);
+    return one(&m.out[i], g.out, g.ld_out, 32) && one(&m.u_a, u, g.ld_u, 32) && one(&m.u_b, u ? u + g.N : u, g.ld_u, 32) &&
            one(&m.du_a, du, g.ld_du, 32) && one(&m.du_b, du ? du + g.N : du, g.ld_du, 32);
 }
 
-// Tile shape of a product and how its last tiles are shared out, from its sizes alone.
+// Tile shape of a launch and how its last tiles are shared out, from its products' sizes alone.
 struct Plan {
-    int shape;
-    int32_t tiles_m, tiles_n, kblocks;
-    int64_t tiles, whole;
+    int shape, n;
     int32_t pieces, piece_kb;
+    struct One {
+        int32_t tiles_m, tiles_n, kblocks;
+        int64_t tiles, whole;
+    } g[ffn::MAX_PRODUCTS];
+    int64_t rest, rest_kb;
 };
 
 // What a shape costs, in microseconds, from runs of all shapes at some twenty sizes (d 64 to
@@ -931,25 +989,42 @@ struct ShapeCost {
 };
 constexpr ShapeCost kCost[3] = {{4.0, 0.25, 0.43, 1.0, 0.0}, {6.0, 0.31, 0.43, 2.5, 0.0}, {9.0, 0.60, 0.70, 2.5, 4.0}};
 
-// The cheaper way to share out the last tiles of a shape; returns the product's cost.
+// The cheaper way to share out the last tiles of a shape; returns the launch's cost.
 double share_out(Plan& r, const ShapeCost& c, int64_t workers, double slot_mb)
 {
-    const auto kb_time = [&](int64_t active) { return std::max(c.kb_few, c.kb_busy * (double)active / (double)workers); };
-    const int64_t rest = r.tiles % workers, q = rest * r.kblocks;
-    r.whole = r.tiles;
+    const auto kb_time = [&](int64_t active) {
+        return std::max(c.kb_few, c.kb_busy * (double)std::min(active, workers) / (double)workers);
+    };
+    double cost = c.launch;
+    r.rest = r.rest_kb = 0;
     r.pieces = r.piece_kb = 0;
-    double cost = c.launch + (double)(r.tiles / workers) * (std::max(r.kblocks * c.kb_busy, c.tile) + c.alone);
-    if (!rest) return cost;
-    double best = r.kblocks * kb_time(rest) + c.tile;
-    const int64_t least = (q + workers - 1) / workers;
-    for (int s = 2; s <= 32 && s <= r.kblocks; ++s) {
-        const int64_t kb = std::max<int64_t>(least, (r.kblocks + s - 1) / s), pieces = (q + kb - 1) / kb;
+    for (int i = 0; i < r.n; ++i) {
+        Plan::One& g = r.g[i];
+        const int64_t rest = g.tiles % workers;
+        g.whole = g.tiles - rest;
+        cost += (double)(g.tiles / workers) * (std::max(g.kblocks * c.kb_busy, c.tile) + c.alone);
+        r.rest += rest;
+        r.rest_kb += rest * g.kblocks;
+    }
+    if (!r.rest) return cost;
+    // whole tiles, the longest first: a round takes as long as its first tile
+    double best = 0;
+    int64_t seen = 0, round = 0;
+    for (int i = 0; i < r.n; ++i) {
+        seen += r.g[i].tiles - r.g[i].whole;
+        for (; round < seen; round += workers)
+            best += std::max(r.g[i].kblocks * kb_time(r.rest - round), c.tile) + c.alone;
+    }
+    best += c.tile;
+    const int64_t least = (r.rest_kb + workers - 1) / workers;
+    for (int s : {2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+        if (s > r.g[0].kblocks) break;
+        const int64_t kb = std::max<int64_t>(least, (r.g[0].kblocks + s - 1) / s), pieces = (r.rest_kb + kb - 1) / kb;
         // the join: its launch, a tile's pieces one after another, the slots written and read
-        const double join = 3.0 + 0.15 * (double)((pieces + rest - 1) / rest) + 2.0 * slot_mb * (double)pieces / 5.0;
-        const double t = (double)kb * kb_time(pieces) + c.tile + join;
+        const double join = 3.0 + 0.15 * (double)((pieces + r.rest - 1) / r.rest) + 2.0 * slot_mb * (double)pieces / 5.0;
+        const double t = (double)kb * kb_time(pieces) + c.tile + c.alone + join;
         if (t < best) {
             best = t;
-            r.whole = r.tiles - rest;
             r.pieces = (int32_t)pieces;
             r.piece_kb = (int32_t)kb;
         }
@@ -957,21 +1032,28 @@ double share_out(Plan& r, const ShapeCost& c, int64_t workers, double slot_mb)
     return cost + best;
 }
 
-Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
+// The products of a launch must be in the order of K, longest first.
+Plan plan(const FfnProduct* p, int n)
 {
     Plan best{};
     double cost = 0;
+    int64_t most = 0;
+    for (int i = 0; i < n; ++i) most = std::max(most, p[i].M);
     for (int shape = ffn::SINGLE; shape <= ffn::WIDE; ++shape) {
-        if ((shape == ffn::PAIR && M <= 128) || (shape == ffn::WIDE && (M <= 256 || epi == FFN_DACT))) continue;
+        if ((shape == ffn::PAIR && most <= 128) || (shape == ffn::WIDE && (most <= 256 || p[0].epi == FFN_DACT))) continue;
         Plan r{};
         r.shape = shape;
+        r.n = n;
         const int64_t tm = shape == ffn::SINGLE ? 128 : shape == ffn::PAIR ? 256 : 512;
-        const int64_t tw = shape == ffn::SINGLE ? 128 : 256, tn = epi == FFN_UP ? tw / 2 : tw;
-        r.kblocks = (int32_t)((K + ffn::BK - 1) / ffn::BK);
-        r.tiles_m = (int32_t)((M + tm - 1) / tm);
-        r.tiles_n = (int32_t)((N + tn - 1) / tn);
-        r.tiles = (int64_t)r.tiles_m * r.tiles_n;
-        const double slot_mb = (double)std::min(M, tm) * (double)tw * 4e-6;
+        const int64_t tw = shape == ffn::SINGLE ? 128 : 256, tn = p[0].epi == FFN_UP ? tw / 2 : tw;
+        for (int i = 0; i < n; ++i) {
+            Plan::One& g = r.g[i];
+            g.kblocks = (int32_t)((p[i].K + ffn::BK - 1) / ffn::BK);
+            g.tiles_m = (int32_t)((p[i].M + tm - 1) / tm);
+            g.tiles_n = (int32_t)((p[i].N + tn - 1) / tn);
+            g.tiles = (int64_t)g.tiles_m * g.tiles_n;
+        }
+        const double slot_mb = (double)std::min(most, tm) * (double)tw * 4e-6;
         const double c = share_out(r, kCost[shape], shape == ffn::SINGLE ? ffn::B200_SMS : ffn::B200_SMS / 2, slot_mb);
         if (!cost || c < cost) {
             best = r;
@@ -981,10 +1063,10 @@ Plan plan(FfnEpi epi, int64_t M, int64_t N, int64_t K)
     return best;
 }
 
-template <int MODE, bool A_MN, bool B_MN, int S>
+template <int MODE, bool B_MN, int S>
 cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
 {
-    auto kern = ffn::k_product<MODE, A_MN, B_MN, S>;
+    auto kern = ffn::k_product<MODE, B_MN, S>;
     constexpr bool PAIRED = ffn::Tile<S>::PAIRED;
     constexpr int kMaxDevices = 64;
     static int workers_dev[kMaxDevices] = {};  // resident CTAs or pairs, once the attribute is set
@@ -1024,108 +1106,110 @@ cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool afte
         }
         workers = workers_dev[dev];
     }
-    workers = std::min<int64_t>(std::max<int64_t>(p.whole, p.pieces), workers);
+    int64_t items = p.pieces ? p.pieces : p.rest_tiles;
+    for (int i = 0; i < p.n; ++i) items = std::max(items, p.g[i].whole);
+    workers = std::min(items, workers);
     cfg.gridDim = dim3((unsigned)(PAIRED ? 2 * workers : workers));
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
-}
-
-template <int MODE, bool A_MN, bool B_MN>
-cudaError_t launch_shape(int shape, const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
-{
-    if (shape == ffn::SINGLE) return launch_kernel<MODE, A_MN, B_MN, ffn::SINGLE>(maps, p, after, s);
-    if (shape == ffn::PAIR) return launch_kernel<MODE, A_MN, B_MN, ffn::PAIR>(maps, p, after, s);
-    if constexpr (MODE != ffn::DACT) return launch_kernel<MODE, A_MN, B_MN, ffn::WIDE>(maps, p, after, s);
-    return cudaErrorInvalidValue;
 }
 
 template <int MODE, int S> cudaError_t launch_join(const ffn::Params& p, cudaStream_t s)
 {
     // a warp takes 4 rows x up to 128 columns of one tile
-    const int64_t warps = (std::min<int64_t>(p.M, ffn::Tile<S>::M) + 3) / 4 *
+    int64_t most = 0;
+    for (int i = 0; i < p.n; ++i) most = std::max<int64_t>(most, p.g[i].M);
+    const int64_t warps = (std::min<int64_t>(most, ffn::Tile<S>::M) + 3) / 4 *
                           std::max(1, ffn::Tile<S>::N / (MODE == ffn::UP ? 256 : 128));
     cudaLaunchAttribute la[1];
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     la[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(256);
-    cfg.gridDim = dim3((unsigned)((warps + 7) / 8), (unsigned)(p.tiles - p.whole));
+    cfg.gridDim = dim3((unsigned)((warps + 7) / 8), (unsigned)p.rest_tiles);
     cfg.stream = s;
     cfg.attrs = la;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, ffn::k_join<MODE, S>, p);
 }
 
-template <int MODE> cudaError_t launch_join(int shape, const ffn::Params& p, cudaStream_t s)
+template <int MODE, bool B_MN, int S>
+cudaError_t launch_both(const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
 {
-    return shape == ffn::SINGLE ? launch_join<MODE, ffn::SINGLE>(p, s)
-           : shape == ffn::PAIR ? launch_join<MODE, ffn::PAIR>(p, s)
-                                : launch_join<MODE, ffn::WIDE>(p, s);
+    const cudaError_t e = launch_kernel<MODE, B_MN, S>(maps, p, after, s);
+    return e != cudaSuccess || !p.pieces ? e : launch_join<MODE, S>(p, s);
+}
+
+template <int MODE, bool B_MN>
+cudaError_t launch_shape(int shape, const ffn::Maps& maps, const ffn::Params& p, bool after, cudaStream_t s)
+{
+    if (shape == ffn::SINGLE) return launch_both<MODE, B_MN, ffn::SINGLE>(maps, p, after, s);
+    if (shape == ffn::PAIR) return launch_both<MODE, B_MN, ffn::PAIR>(maps, p, after, s);
+    if constexpr (MODE != ffn::DACT) return launch_both<MODE, B_MN, ffn::WIDE>(maps, p, after, s);
+    return cudaErrorInvalidValue;
 }
 
 bool on32(const void* p, int64_t ld, int64_t esz) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld * esz % 32 == 0; }
 
 }  // namespace
 
-size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K)
+size_t ffn_slot_bytes(int64_t rows)
 {
-    const Plan r = plan(epi, M, N, K);
-    return (size_t)r.pieces * 2 * (r.shape == ffn::SINGLE ? 128 * 128 : r.shape == ffn::PAIR ? 256 * 256 : 512 * 256) * 4;
+    // two slots a worker: 148 CTAs with 128 x 128, 74 pairs with 256 x 256 or 512 x 256
+    const size_t one = rows <= 128 ? 2 * 128 * 128 : rows <= 256 ? 256 * 256 : 512 * 256;
+    return 2 * (ffn::B200_SMS / 2) * one * 4;
 }
 
-cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s)
+cudaError_t launch_ffn_products(FfnProduct* g, int n, bool after, cudaStream_t s)
 {
+    std::sort(g, g + n, [](const FfnProduct& a, const FfnProduct& b) { return a.K > b.K; });
+    const Plan r = plan(g, n);
     ffn::Maps maps;
-    const Plan r = plan(g.epi, g.M, g.N, g.K);
     ffn::Params p{};
-    if (r.tiles >= (int64_t)1 << 31) {
-        record_error("the product has more than 2^31 tiles");
-        return cudaErrorInvalidValue;
-    }
-    int32_t a_rows = r.shape == ffn::WIDE ? 2 * ffn::BM : ffn::BM;
-    if (r.shape == ffn::SINGLE && !g.a_mn && r.tiles_m == 1) a_rows = (int32_t)((g.M + 7) / 8 * 8);
-    if (a_rows == ffn::BOX) a_rows += 8;  // 64 means two boxes
-    p.stage_bytes = a_rows * ffn::BK * 2 + ffn::BM * ffn::BK * 2;
-    if (!make_map(&maps.a, g.a, g.a_mn, a_rows, &p.a_blocks) ||
-        !make_map(&maps.b, g.b, g.b_mn, g.epi == FFN_UP && r.shape == ffn::SINGLE ? ffn::BOX : ffn::BM, &p.b_blocks) ||
-        !out_maps(maps, g)) {
-        record_error("tensor map encoding failed (cuTensorMapEncodeTiled unavailable or refused the layout)");
-        return cudaErrorInvalidValue;
-    }
-    p.M = (int32_t)g.M;
-    p.N = (int32_t)g.N;
-    p.kblocks = r.kblocks;
-    p.tiles_m = r.tiles_m;
-    p.tiles_n = r.tiles_n;
-    p.tiles = r.tiles;
-    p.whole = r.whole;
+    p.n = n;
     p.pieces = r.pieces;
     p.piece_kb = r.piece_kb;
-    p.out = g.out;
-    p.ld_out = g.ld_out;
-    p.out_f32 = g.out_f32;
-    p.accumulate = g.accumulate;
-    p.u = static_cast<bf16*>(g.u);
-    p.ld_u = g.ld_u;
-    p.du = static_cast<bf16*>(g.du);
-    p.ld_du = g.ld_du;
-    p.slots = g.slots;
-    p.wide = on32(g.out, g.ld_out, g.out_f32 ? 4 : 2) && on32(g.u, g.ld_u, 2) && on32(g.du, g.ld_du, 2) &&
-             (g.epi == FFN_STORE || g.N % 16 == 0);
-    cudaError_t e;
-    if (g.epi == FFN_UP)
-        e = launch_shape<ffn::UP, false, false>(r.shape, maps, p, after, s);
-    else if (g.epi == FFN_DACT)
-        e = launch_shape<ffn::DACT, false, true>(r.shape, maps, p, after, s);
-    else if (g.a_mn)  // dW: both operands with M, N contiguous
-        e = launch_shape<ffn::STORE, true, true>(r.shape, maps, p, after, s);
-    else if (g.b_mn)  // dx
-        e = launch_shape<ffn::STORE, false, true>(r.shape, maps, p, after, s);
-    else  // y
-        e = launch_shape<ffn::STORE, false, false>(r.shape, maps, p, after, s);
-    if (e != cudaSuccess || !r.pieces) return e;
-    if (g.epi == FFN_UP) return launch_join<ffn::UP>(r.shape, p, s);
-    if (g.epi == FFN_DACT) return launch_join<ffn::DACT>(r.shape, p, s);
-    return launch_join<ffn::STORE>(r.shape, p, s);
+    p.rest_tiles = r.rest;
+    p.rest_kb = r.rest_kb;
+    p.u = static_cast<bf16*>(g[0].u);
+    p.ld_u = g[0].ld_u;
+    p.du = static_cast<bf16*>(g[0].du);
+    p.ld_du = g[0].ld_du;
+    p.slots = g[0].slots;
+    for (int i = 0; i < n; ++i) {
+        ffn::Product& c = p.g[i];
+        if (r.g[i].tiles >= (int64_t)1 << 31) {
+            record_error("the product has more than 2^31 tiles");
+            return cudaErrorInvalidValue;
+        }
+        int32_t a_rows = r.shape == ffn::WIDE ? 2 * ffn::BM : ffn::BM;
+        if (r.shape == ffn::SINGLE && !g[i].a_mn && r.g[i].tiles_m == 1) a_rows = (int32_t)((g[i].M + 7) / 8 * 8);
+        if (a_rows == ffn::BOX) a_rows += 8;  // 64 means two boxes
+        c.stage_bytes = a_rows * ffn::BK * 2 + ffn::BM * ffn::BK * 2;
+        const int32_t b_rows = g[i].epi == FFN_UP && r.shape == ffn::SINGLE ? ffn::BOX : ffn::BM;
+        if (!make_map(&maps.a[i], g[i].a, g[i].a_mn, a_rows, &c.a_blocks) ||
+            !make_map(&maps.b[i], g[i].b, g[i].b_mn, b_rows, &c.b_blocks) || !out_maps(maps, i, g[i])) {
+            record_error("tensor map encoding failed (cuTensorMapEncodeTiled unavailable or refused the layout)");
+            return cudaErrorInvalidValue;
+        }
+        c.M = (int32_t)g[i].M;
+        c.N = (int32_t)g[i].N;
+        c.kblocks = r.g[i].kblocks;
+        c.tiles_m = r.g[i].tiles_m;
+        c.tiles_n = r.g[i].tiles_n;
+        c.tiles = r.g[i].tiles;
+        c.whole = r.g[i].whole;
+        c.a_mn = g[i].a_mn;
+        c.out = g[i].out;
+        c.ld_out = g[i].ld_out;
+        c.out_f32 = g[i].out_f32;
+        c.accumulate = g[i].accumulate;
+        c.wide = on32(c.out, c.ld_out, c.out_f32 ? 4 : 2) && on32(p.u, p.ld_u, 2) && on32(p.du, p.ld_du, 2) &&
+                 (g[i].epi == FFN_STORE || c.N % 16 == 0);
+    }
+    if (g[0].epi == FFN_UP) return launch_shape<ffn::UP, false>(r.shape, maps, p, after, s);
+    if (g[0].epi == FFN_DACT) return launch_shape<ffn::DACT, true>(r.shape, maps, p, after, s);
+    if (g[0].b_mn) return launch_shape<ffn::STORE, true>(r.shape, maps, p, after, s);
+    return launch_shape<ffn::STORE, false>(r.shape, maps, p, after, s);
 }
 
 uint32_t ffn_device_error(bool clear)

@@ -114,8 +114,8 @@ sol_status check_ffn_sizes(int64_t n_tokens, int64_t d, int64_t inner, sol_dtype
     return SOL_OK;
 }
 
-// Workspace: act [T, inner], du [T, 2 * inner] (bf16), then the f32 slots of whichever
-// product needs most (the products run one after another).
+// Workspace: act [T, inner], du [T, 2 * inner] (bf16), then the f32 slots of one launch (the
+// launches run one after another).
 struct FfnWorkspace {
     size_t act, du, slots, total;
 };
@@ -126,14 +126,7 @@ FfnWorkspace ffn_layout(int64_t T, int64_t d, int64_t inner)
     w.act = 0;
     w.du = up256((size_t)T * (size_t)inner * 2);
     w.slots = up256(w.du + (size_t)T * (size_t)inner * 4);
-    size_t most = 0;
-    if (T > 0)
-        for (size_t b : {sol::ffn_slot_bytes(sol::FFN_UP, T, inner, d), sol::ffn_slot_bytes(sol::FFN_STORE, T, d, inner),
-                         sol::ffn_slot_bytes(sol::FFN_DACT, T, inner, d),
-                         sol::ffn_slot_bytes(sol::FFN_STORE, T, d, 2 * inner),
-                         sol::ffn_slot_bytes(sol::FFN_STORE, 2 * inner, d, T),
-                         sol::ffn_slot_bytes(sol::FFN_STORE, d, inner, T)})
-            most = std::max(most, b);
+    const size_t most = T > 0 ? sol::ffn_slot_bytes(std::max({T, d, 2 * inner})) : 0;
     w.total = up256(w.slots + most);
     return w;
 }
@@ -203,10 +196,10 @@ sol_status sol_ffn(void* y, int64_t ld_y, void* u, int64_t ld_u, const void* x, 
                                 act, inner, workspace, lay);
     g.u = u;
     g.ld_u = ld_u;
-    TRY(cuda_status(sol::launch_ffn_product(g, false, s), "sol_ffn up projection launch"));
+    TRY(cuda_status(sol::launch_ffn_products(&g, 1, false, s), "sol_ffn up projection launch"));
     g = product(sol::FFN_STORE, T, d, inner, {act, T, inner, inner}, false, {w_down, d, inner, ld_wd}, false, y, ld_y,
                 workspace, lay);
-    return cuda_status(sol::launch_ffn_product(g, true, s), "sol_ffn down projection launch");
+    return cuda_status(sol::launch_ffn_products(&g, 1, true, s), "sol_ffn down projection launch");
 }
 
 sol_status sol_ffn_backward(void* dx, int64_t ld_dx, void* dw_up, int64_t ld_dwu, void* dw_down, int64_t ld_dwd,
@@ -255,27 +248,23 @@ sol_status sol_ffn_backward(void* dx, int64_t ld_dx, void* dw_up, int64_t ld_dwu
     g.ld_u = ld_u;
     g.du = du;
     g.ld_du = 2 * inner;
-    TRY(cuda_status(sol::launch_ffn_product(g, false, s), "sol_ffn_backward d_act launch"));
-    if (dw_down) {
-        g = product(sol::FFN_STORE, d, inner, T, {dy, T, d, ld_dy}, true, {act, T, inner, inner}, true, dw_down, ld_dwd,
-                    workspace, lay);
-        g.out_f32 = grad_dt == SOL_DTYPE_F32;
-        g.accumulate = accumulate != 0;
-        TRY(cuda_status(sol::launch_ffn_product(g, true, s), "sol_ffn_backward dw_down launch"));
+    TRY(cuda_status(sol::launch_ffn_products(&g, 1, false, s), "sol_ffn_backward d_act launch"));
+    sol::FfnProduct all[3];
+    int n = 0;
+    if (dx)
+        all[n++] = product(sol::FFN_STORE, T, d, 2 * inner, {du, T, 2 * inner, 2 * inner}, false, {w_up, 2 * inner, d, ld_wu},
+                           true, dx, ld_dx, workspace, lay);
+    if (dw_up)
+        all[n++] = product(sol::FFN_STORE, 2 * inner, d, T, {du, T, 2 * inner, 2 * inner}, true, {x, T, d, ld_x}, true,
+                           dw_up, ld_dwu, workspace, lay);
+    if (dw_down)
+        all[n++] = product(sol::FFN_STORE, d, inner, T, {dy, T, d, ld_dy}, true, {act, T, inner, inner}, true, dw_down,
+                           ld_dwd, workspace, lay);
+    for (int i = dx ? 1 : 0; i < n; ++i) {
+        all[i].out_f32 = grad_dt == SOL_DTYPE_F32;
+        all[i].accumulate = accumulate != 0;
     }
-    if (dw_up) {
-        g = product(sol::FFN_STORE, 2 * inner, d, T, {du, T, 2 * inner, 2 * inner}, true, {x, T, d, ld_x}, true, dw_up,
-                    ld_dwu, workspace, lay);
-        g.out_f32 = grad_dt == SOL_DTYPE_F32;
-        g.accumulate = accumulate != 0;
-        TRY(cuda_status(sol::launch_ffn_product(g, true, s), "sol_ffn_backward dw_up launch"));
-    }
-    if (dx) {
-        g = product(sol::FFN_STORE, T, d, 2 * inner, {du, T, 2 * inner, 2 * inner}, false, {w_up, 2 * inner, d, ld_wu},
-                    true, dx, ld_dx, workspace, lay);
-        TRY(cuda_status(sol::launch_ffn_product(g, true, s), "sol_ffn_backward dx launch"));
-    }
-    return SOL_OK;
+    return cuda_status(sol::launch_ffn_products(all, n, true, s), "sol_ffn_backward gradients launch");
 }
 
 // ---------------------------------------------------------------------------------

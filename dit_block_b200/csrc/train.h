@@ -36,13 +36,15 @@ struct FfnProduct {
     int64_t ld_u;
     void* du;          // FFN_DACT
     int64_t ld_du;
-    float* slots;      // workspace of ffn_slot_bytes
+    float* slots;      // workspace of ffn_slot_bytes (of a launch's products one and the same)
 };
 
-// Bytes of f32 slots the product needs for the tiles that several workers share.
-size_t ffn_slot_bytes(FfnEpi epi, int64_t M, int64_t N, int64_t K);
-// after: the kernel before on the stream is one of the same call, which may still be ending.
-cudaError_t launch_ffn_product(const FfnProduct& g, bool after, cudaStream_t s);
+// Bytes of f32 slots for the tiles that several workers share, for products of up to `rows` rows.
+size_t ffn_slot_bytes(int64_t rows);
+// One launch (and one to join what several workers share) of n products: one FFN_UP or FFN_DACT, or up to three
+// FFN_STORE with B of one layout that do not depend on each other.  Reorders g.  after: the kernel
+// before on the stream is one of the same call, which may still be ending.
+cudaError_t launch_ffn_products(FfnProduct* g, int n, bool after, cudaStream_t s);
 
 // The whole forward pass for a few tokens (k_ffn_small.cu).  Measured at d x inner, us, against
 // k_ffn.cu:   1 token   5120 x 13824  69.8 : 83.5    1000 x 2504   6.0 : 19.0

@@ -32,7 +32,7 @@ extern "C" {
  * between calls; calls that may overlap on the GPU need one each, and a captured graph
  * keeps using the one it was captured with.
  * Results do not depend on timing: work split over the inner dimension is joined in a
- * fixed order.
+ * fixed order, which depends on the sizes and on which gradients are asked for.
  * ------------------------------------------------------------------------------------ */
 size_t sol_ffn_workspace_bytes(int64_t n_tokens, int64_t d, int64_t inner);
 
