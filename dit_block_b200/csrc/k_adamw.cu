@@ -549,6 +549,7 @@ __global__ void __launch_bounds__(THREADS, 8) k_norm_partial(const AdamwTable t,
 {
     __shared__ double buf[THREADS / 32];
     double sum = 0.0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int64_t b = blockIdx.x; b < t.n_chunks; b += gridDim.x) {
         const AdamwChunk c = t.chunks[b];
         const AdamwTensor* x = t.tensors + c.tensor;
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_final(float* out, const double
 {
     __shared__ double buf[THREADS / 32];
     double sum = 0.0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // set up while k_norm_partial ends
     for (int i = threadIdx.x; i < n; i += THREADS) sum += partial[i];
     sum = cta_sum(sum, buf);
     if (threadIdx.x == 0) {
@@ -673,8 +675,16 @@ cudaError_t launch_adamw_grad_norm(float* out, const AdamwTable& t, sol_dtype gr
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    adamw::k_norm_final<<<1, adamw::THREADS, 0, s>>>(out, partial, grid, max_norm);
-    return cudaGetLastError();
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(adamw::THREADS);
+    cfg.stream = s;
+    cfg.attrs = la;
+    cfg.numAttrs = grid > 0 ? 1 : 0;  // behind k_norm_partial alone
+    return cudaLaunchKernelEx(&cfg, adamw::k_norm_final, out, (const double*)partial, grid, max_norm);
 }
 
 cudaError_t launch_adamw_decode(void* m_out, void* v_out, sol_dtype out_dt, const void* m, const void* v,

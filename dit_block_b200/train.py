@@ -7,7 +7,6 @@ device unless ``stream`` is given; every tensor of a call lies on one CUDA devic
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -63,9 +62,17 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _on(index: int):
-    """Makes a device the current one for a call."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
+def _call(name: str, device: int, stream, *args):
+    """Calls a function whose last argument is the stream, with `device` the current one."""
+    fn = getattr(_lib or lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(device) if stream is None else sol._stream(stream)
+    if torch.cuda.current_device() == device:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        sol._check(status, name)
 
 
 def _device(t) -> int:
@@ -123,8 +130,7 @@ def ffn(y, x, w_up, w_down, *, u=None, workspace, stream=None):
     args = (*_matrix("y", y, n, d, bf, dev), *(_NONE if u is None else _matrix("u", u, n, 2 * inner, bf, dev)),
             *_matrix("x", x, n, d, bf, dev), *_matrix("w_up", w_up, 2 * inner, d, bf, dev),
             *_matrix("w_down", w_down, d, inner, bf, dev), *_space(workspace, dev), n, d, inner, sol.BF16)
-    with _on(dev):
-        sol._check((_lib or lib()).sol_ffn(*args, sol._stream(stream)), "sol_ffn")
+    _call("sol_ffn", dev, stream, *args)
     return y
 
 
@@ -147,8 +153,7 @@ def ffn_backward(dy, x, u, w_up, w_down, *, dx=None, dw_up=None, dw_down=None, a
             *_matrix("x", x, n, d, bf, dev), *_matrix("u", u, n, 2 * inner, bf, dev),
             *_matrix("w_up", w_up, 2 * inner, d, bf, dev), *_matrix("w_down", w_down, d, inner, bf, dev),
             *_space(workspace, dev), n, d, inner, sol.BF16)
-    with _on(dev):
-        sol._check((_lib or lib()).sol_ffn_backward(*args, sol._stream(stream)), "sol_ffn_backward")
+    _call("sol_ffn_backward", dev, stream, *args)
 
 
 # ---------------------------------------------------------------------------------- AdamW
@@ -199,7 +204,7 @@ class AdamW:
         self.device = torch.device("cuda", dev)
         self._index = dev
         h = _P()
-        with _on(dev):
+        with torch.cuda.device(dev):
             sol._check(lib().sol_adamw_plan_create(ctypes.byref(h), rows, n,
                                                    sol.BF16 if grad_type == torch.bfloat16 else sol.F32, bits),
                        "sol_adamw_plan_create")
@@ -214,8 +219,7 @@ class AdamW:
                          None if lr_device is None else _flat("lr_device", lr_device, 1, torch.float32, dev),
                          None if step_device is None else _flat("step_device", step_device, 1, torch.int64, dev),
                          None if grad_factor is None else _flat("grad_factor", grad_factor, 1, torch.float32, dev))
-        with _on(dev):
-            sol._check(_lib.sol_adamw_step(self._handle, ctypes.byref(h), sol._stream(stream)), "sol_adamw_step")
+        _call("sol_adamw_step", dev, stream, self._handle, ctypes.byref(h))
 
     def norm_workspace(self) -> torch.Tensor:
         """A workspace for grad_norm (one for each of the calls that may overlap)."""
@@ -224,16 +228,15 @@ class AdamW:
     def grad_norm(self, out, max_norm, *, workspace, stream=None):
         """out[0] = norm of all gradients, out[1] = min(1, max_norm / (out[0] + 1e-6))  (sol_adamw_grad_norm)."""
         dev = self._index
-        args = (_flat("out", out, 2, torch.float32, dev), self._handle, max_norm, *_space(workspace, dev))
-        with _on(dev):
-            sol._check(_lib.sol_adamw_grad_norm(*args, sol._stream(stream)), "sol_adamw_grad_norm")
+        _call("sol_adamw_grad_norm", dev, stream, _flat("out", out, 2, torch.float32, dev), self._handle, max_norm,
+              *_space(workspace, dev))
         return out
 
     def close(self):
         """Frees the plan: its steps have ended, and no captured graph that uses it is replayed any more."""
         if self._handle:
             h, self._handle = self._handle, None
-            with _on(self._index):
+            with torch.cuda.device(self._index):
                 sol._check(lib().sol_adamw_plan_destroy(h), "sol_adamw_plan_destroy")
             self._kept = None
 
@@ -267,6 +270,4 @@ def adamw_state_decode(m_out, v_out, m, v, m_scale, v_scale, *, stream=None):
 
     mo, mq, ms = part("m", m_out, m, m_scale, torch.int8)
     vo, vq, vs = part("v", v_out, v, v_scale, torch.uint8)
-    with _on(dev):
-        sol._check((_lib or lib()).sol_adamw_state_decode(mo, vo, sol._dtype(out), mq, vq, ms, vs, n, sol._stream(stream)),
-                   "sol_adamw_state_decode")
+    _call("sol_adamw_state_decode", dev, stream, mo, vo, sol._dtype(out), mq, vq, ms, vs, n)
