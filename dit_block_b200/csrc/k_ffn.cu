@@ -570,6 +570,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
     const uint32_t u_bar = smem_u32(&b->u_full[(warp - EPI_WARP0) & 7]);
     uint32_t u_phase = 0;
     bool u_pending = false, ok = true;
+    int turn = 0;  // the box that is written next
     int64_t n = 0;
     Walk walk = walk_begin(w.worker);
     Piece it;
@@ -629,9 +630,9 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                     }
                     continue;
                 }
-                // boxes of 64 columns in turn
+                // boxes of 64 columns in turn, from tile to tile
                 constexpr int BOXES = SPACE / BOX64;
-                const uint32_t dst = box + (c / 2 % BOXES) * BOX64;
+                const uint32_t dst = box + turn * BOX64;
                 if (!(c & 1)) {
                     if (lane == 0) tc::bulk_wait_read<BOXES - 1>();
                     __syncwarp();
@@ -645,6 +646,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                         tc::tma_store_2d(&maps.out[it.g], dst, col - 32 * (c & 1), row0);
                         tc::bulk_commit();
                     }
+                    turn = turn + 1 == BOXES ? 0 : turn + 1;
                 }
             } else if constexpr (MODE == UP && SPACE < 3 * BOX32) {
                 // two boxes: a and b, then act in the first of them; act alone takes them in turn
@@ -666,7 +668,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = v[e] * sigmoid_fast(v[e]) * g[e];
-                const uint32_t dst = p.u ? box : box + (c & 1) * BOX32;
+                const uint32_t dst = p.u ? box : box + turn * BOX32;
                 if (lane == 0) {
                     if (p.u)
                         tc::bulk_wait_read<0>();
@@ -682,6 +684,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                     tc::tma_store_2d(&maps.out[it.g], dst, col, row0);
                     tc::bulk_commit();
                 }
+                turn ^= 1;
             } else if constexpr (MODE == UP) {
                 if (lane == 0) tc::bulk_wait_read<0>();
                 __syncwarp();

@@ -23,7 +23,8 @@ HALF, ACC, FN = 2.0 ** -8, 2.0 ** -23, 2.0 ** -20
 SIZES = [  # n_tokens, d, inner
     (1, 8, 8), (1, 256, 512), (2, 64, 128), (7, 72, 1032), (31, 264, 136), (8, 136, 72), (9, 520, 264), (16, 64, 8200), (16, 1000, 336), (17, 72, 80), (57, 64, 72),
     (63, 128, 64), (64, 128, 64), (65, 72, 64), (120, 64, 128), (128, 256, 512),
-    (129, 64, 200), (257, 1000, 328), (1000, 200, 2504), (4099, 64, 64), (300, 2560, 1024),
+    (129, 64, 200), (257, 1000, 328), (1000, 200, 2504), (4099, 64, 64), (300, 2560, 1024), (20, 2000, 6008),
+    (600, 1536, 4104),
 ]
 
 
@@ -243,7 +244,7 @@ def test_a_nan_stays_in_its_token():
     assert y[77].isnan().all() and u[77].isnan().all()
 
 
-@pytest.mark.parametrize("n,d,inner", [(1, 256, 512), (200, 264, 520), (5000, 64, 64)])
+@pytest.mark.parametrize("n,d,inner", [(1, 256, 512), (200, 264, 520), (5000, 64, 64), (9, 4096, 8192), (700, 2048, 4096)])
 def test_the_same_bits_every_time_and_on_another_stream(n, d, inner):
     i = inputs(n, d, inner)
     dy = drawn(4, n, d, 0.1)
