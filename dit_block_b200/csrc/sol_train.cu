@@ -346,6 +346,8 @@ try {
         if (e == cudaSuccess)
             e = cudaMemcpy((char*)r->dev + at, chunks.data(), chunks.size() * sizeof(sol::AdamwChunk),
                            cudaMemcpyHostToDevice);
+        // a copy from pageable memory may still be on its way, and steps may run on any stream
+        if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     }
     if (e != cudaSuccess) {
         if (r->dev) cudaFree(r->dev);

@@ -109,7 +109,8 @@ typedef struct {
 } sol_adamw_scalars;
 
 /* A plan holds the tensors' addresses on the current device (one allocation, made here and
- * freed by destroy; a captured graph that uses it must not outlive it).  `tensors` is a host
+ * freed by destroy, neither inside a stream capture; a captured graph that uses the plan must
+ * not outlive it).  `tensors` is a host
  * array, copied.  Every pointer is 16-byte aligned; no written buffer may overlap another
  * buffer of the plan.  grad_dt: SOL_DTYPE_F32 or SOL_DTYPE_BF16, of all gradients. */
 typedef struct sol_adamw_plan sol_adamw_plan;
