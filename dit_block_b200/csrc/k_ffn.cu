@@ -750,9 +750,9 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                 tc::mbar_arrive(e);
         }
     }
-    // copies in and out of this warp's boxes end before its CTA does
+    // copies into this warp's boxes, and the reads of those out of them, end before its CTA does
     if (MODE == DACT && u_pending && !mbar_wait_bounded(u_bar, u_phase, kWaitLimit)) atomicOr(&g_error, 64u);
-    if (lane == 0) tc::bulk_wait_all();
+    if (lane == 0) tc::bulk_wait_read<0>();
     __syncwarp();
 }
 

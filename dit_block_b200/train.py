@@ -84,7 +84,7 @@ def _device(t) -> int:
 
 def _matrix(name: str, t, rows: int, cols: int, dtype, device: int):
     """(address, row stride) of a [rows, cols] argument; a single row may have any stride."""
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
