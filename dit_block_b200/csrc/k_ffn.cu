@@ -74,8 +74,6 @@ template <int S> struct Tile {
     static constexpr int ROWS = BM * HALVES;          // rows of a CTA
     static constexpr int M = PAIRED ? 2 * ROWS : ROWS, N = PAIRED ? 256 : 128;
     static constexpr int A_BYTES = ROWS * BK * 2, STAGE_BYTES = A_BYTES + 128 * BK * 2;
-    static constexpr int STAGES = S == WIDE ? 4 : 5;  // PAIR: as fast as 6 and 7
-    static constexpr int EPI_BYTES = S == WIDE ? 32768 : 49152;  // staging of the epilogue warps
     static constexpr int ACCS = S == WIDE ? 1 : 2;    // accumulators in TMEM
     static constexpr int TMEM_COLS = S == SINGLE ? 256 : 512;
 };
@@ -86,6 +84,14 @@ constexpr int MAX_STAGES = 5;
 // per quarter, half of the rows each).
 __host__ __device__ constexpr int epi_warps(int mode, int shape) { return mode != STORE || shape == WIDE ? 8 : 4; }
 __host__ __device__ constexpr int block_threads(int mode, int shape) { return 64 + 32 * epi_warps(mode, shape); }
+// Staging of the epilogue warps, and stages of the ring in what is left (PAIR: five are as fast as
+// seven; d_act with four took 162 us of 152 for 1,252 tokens at full width).  A SINGLE tile of d_act
+// brings all of its u at once.
+__host__ __device__ constexpr int epi_bytes(int mode, int shape)
+{
+    return shape == WIDE ? 32768 : mode == DACT && shape == SINGLE ? 98304 : 49152;
+}
+__host__ __device__ constexpr int stages(int mode, int shape) { return shape == WIDE || (mode == DACT && shape == SINGLE) ? 4 : 5; }
 
 struct Bars {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drain;
@@ -94,11 +100,12 @@ struct Bars {
     uint32_t tmem_base;
     volatile int32_t abort;
 };
-template <int S> constexpr size_t smem_bytes()
+template <int MODE, int S> constexpr size_t smem_bytes()
 {
-    return 1024 + (size_t)Tile<S>::STAGES * Tile<S>::STAGE_BYTES + Tile<S>::EPI_BYTES + sizeof(Bars);
+    return 1024 + (size_t)stages(MODE, S) * Tile<S>::STAGE_BYTES + epi_bytes(MODE, S) + sizeof(Bars);
 }
-static_assert(smem_bytes<WIDE>() <= 232448 && smem_bytes<PAIR>() <= 232448, "shared memory of a CTA");
+static_assert(smem_bytes<STORE, WIDE>() <= 232448 && smem_bytes<UP, PAIR>() <= 232448 && smem_bytes<DACT, SINGLE>() <= 232448,
+              "shared memory of a CTA");
 
 __device__ uint32_t g_error;
 
@@ -276,7 +283,7 @@ template <int MODE, bool B_MN, int S>
 __device__ void run_producer(const Maps& maps, const Params& p, uint8_t* ring, Bars* b, const Where& w)
 {
     using T = Tile<S>;
-    constexpr int STAGES = T::STAGES;
+    constexpr int STAGES = stages(MODE, S);
     const bool remote = T::PAIRED && w.rank == 1;
     int s = 0;
     uint32_t phase = 0;
@@ -393,7 +400,7 @@ __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
             } else {
                 tc::commit(e);
             }
-            if (++s == T::STAGES) {
+            if (++s == stages(MODE, S)) {
                 s = 0;
                 phase ^= 1u;
             }
@@ -565,7 +572,7 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, group = (warp - EPI_WARP0) / 4;
     const int half = T::HALVES == 2 ? group : 0, part = T::HALVES == 2 ? 0 : group;
-    constexpr int SPACE = T::EPI_BYTES / EW;  // staging of a warp
+    constexpr int SPACE = epi_bytes(MODE, S) / EW;  // staging of a warp
     const uint32_t box = staging + (warp - EPI_WARP0) * SPACE;
     const uint32_t u_bar = smem_u32(&b->u_full[(warp - EPI_WARP0) & 7]);
     uint32_t u_phase = 0;
@@ -582,12 +589,17 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
         const int32_t row0 = it.m_blk * TM + (int32_t)w.rank * T::ROWS + half * BM + quarter * 32;  // of this warp
         const int32_t col0 = it.n_blk * WIDTH + part * CH * 32;
         const bool whole = it.slot < 0;
+        // DACT: a set of boxes (a, b, act) for each 32 columns whose u is fetched at a time
+        constexpr int SETS = MODE == DACT && S == SINGLE ? CH : 1;
         auto fetch_u = [&](int32_t col) {  // lane 0, once the boxes are free
             if (lane == 0) {
+                const int n = min(SETS, (N - col + 31) / 32);
                 tc::bulk_wait_read<0>();
-                mbar_arrive_expect_tx(u_bar, 2 * BOX32);
-                tc::tma_load_2d(box, &maps.u_a, col, row0, u_bar);
-                tc::tma_load_2d(box + BOX32, &maps.u_b, col, row0, u_bar);
+                mbar_arrive_expect_tx(u_bar, 2 * n * BOX32);
+                for (int i = 0; i < n; ++i) {
+                    tc::tma_load_2d(box + 3 * i * BOX32, &maps.u_a, col + 32 * i, row0, u_bar);
+                    tc::tma_load_2d(box + (3 * i + 1) * BOX32, &maps.u_b, col + 32 * i, row0, u_bar);
+                }
             }
             u_pending = true;
         };
@@ -710,16 +722,19 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                     tc::bulk_commit();
                 }
             } else {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(u_bar, u_phase, kWaitLimit));
-                if (!ok) {
-                    raise_abort(b, 64u);
-                    break;
+                if (c % SETS == 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(u_bar, u_phase, kWaitLimit));
+                    if (!ok) {
+                        raise_abort(b, 64u);
+                        break;
+                    }
+                    u_phase ^= 1u;
+                    u_pending = false;
                 }
-                u_phase ^= 1u;
-                u_pending = false;
+                const uint32_t set = box + (c % SETS) * 3 * BOX32;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t ca = cell64(box, lane, j), cb = cell64(box + BOX32, lane, j);
+                    const uint32_t ca = cell64(set, lane, j), cb = cell64(set + BOX32, lane, j);
                     float fa[8], fb[8];
                     unpack<bf16>(lds16(ca), fa);
                     unpack<bf16>(lds16(cb), fb);
@@ -727,17 +742,17 @@ __device__ void run_epilogue(const Maps& maps, const Params& p, uint32_t staging
                     for (int e = 0; e < 8; ++e) dact_one(v[8 * j + e], fa[e], fb[e]);
                     sts16(ca, pack<bf16>(fa));
                     sts16(cb, pack<bf16>(fb));
-                    sts16(cell64(box + 2 * BOX32, lane, j), pack<bf16>(v + 8 * j));
+                    sts16(cell64(set + 2 * BOX32, lane, j), pack<bf16>(v + 8 * j));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tc::tma_store_2d(&maps.du_a, box, col, row0);
-                    tc::tma_store_2d(&maps.du_b, box + BOX32, col, row0);
-                    if (c0.out) tc::tma_store_2d(&maps.out[it.g], box + 2 * BOX32, col, row0);
+                    tc::tma_store_2d(&maps.du_a, set, col, row0);
+                    tc::tma_store_2d(&maps.du_b, set + BOX32, col, row0);
+                    if (c0.out) tc::tma_store_2d(&maps.out[it.g], set + 2 * BOX32, col, row0);
                     tc::bulk_commit();
                 }
-                if (c + 1 < CH && col + 32 < N) fetch_u(col + 32);
+                if ((c + 1) % SETS == 0 && c + 1 < CH && col + 32 < N) fetch_u(col + 32);
             }
         }
         tc::fence_before_sync();
@@ -763,8 +778,8 @@ __global__ void __launch_bounds__(block_threads(MODE, S), 1)
     using T = Tile<S>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* staging = ring + (size_t)T::STAGES * T::STAGE_BYTES;
-    Bars* b = reinterpret_cast<Bars*>(staging + T::EPI_BYTES);
+    uint8_t* staging = ring + (size_t)stages(MODE, S) * T::STAGE_BYTES;
+    Bars* b = reinterpret_cast<Bars*>(staging + epi_bytes(MODE, S));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Where w;
     w.rank = T::PAIRED ? tc::cluster_rank() : 0u;
@@ -773,7 +788,7 @@ __global__ void __launch_bounds__(block_threads(MODE, S), 1)
 
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int i = 0; i < T::STAGES; ++i) {
+        for (int i = 0; i < stages(MODE, S); ++i) {
             mbar_init(smem_u32(&b->full[i]), 1);
             mbar_init(smem_u32(&b->empty[i]), 1);
             b->peer_last[i] = -1;
@@ -823,7 +838,7 @@ __global__ void __launch_bounds__(block_threads(MODE, S), 1)
         tc::cluster_sync();  // the leader's MMAs have drained; the peer's last phases are in peer_last
         if (w.rank == 0 && threadIdx.x == 0) {
 #pragma unroll
-            for (int i = 0; i < T::STAGES; ++i) {
+            for (int i = 0; i < stages(MODE, S); ++i) {
                 const int32_t ph = b->peer_last[i];
                 if (ph >= 0 && !mbar_wait_bounded(smem_u32(&b->full[i]), (uint32_t)ph, kWaitLimit))
                     atomicOr(&g_error, 2u);
@@ -1087,7 +1102,7 @@ cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool afte
     la[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(ffn::block_threads(MODE, S));
-    cfg.dynamicSmemBytes = ffn::smem_bytes<S>();
+    cfg.dynamicSmemBytes = ffn::smem_bytes<MODE, S>();
     cfg.stream = s;
     cfg.attrs = after ? la : la + 1;
     cfg.numAttrs = (after ? 1 : 0) + (PAIRED ? 1 : 0);
@@ -1095,7 +1110,7 @@ cudaError_t launch_kernel(const ffn::Maps& maps, const ffn::Params& p, bool afte
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!workers_dev[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn::smem_bytes<S>());
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn::smem_bytes<MODE, S>());
             if (e != cudaSuccess) return e;
             int n = sm_count();
             if (PAIRED) {
