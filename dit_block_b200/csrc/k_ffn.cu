@@ -12,8 +12,13 @@
 // swizzle; a box has the contiguous dimension of its operand along its rows, so both
 // layouts cost the same copies and differ only in the matrix descriptor (smem_desc_mn) and
 // the instruction descriptor's major bits.  No operand is transposed in memory.
-// Two shapes: a cluster of two CTAs on a 256 x 256 tile (cta_group::2, each CTA loading
-// half of A and half of B), and one CTA on a 128 x 128 tile where M is at most 128.
+// Three tile shapes (Tile): one CTA on 128 x 128, and a cluster of two CTAs (cta_group::2, each
+// loading half of A and half of B) on 256 x 256 or 512 x 256; plan() takes the one whose estimated
+// time is least.
+//
+// At d 5120, width 13,824 and 31,248 tokens: forward with u kept 10.2 ms (1.30 PFLOP/s), backward
+// 21.5 ms (1.23), both at the power cap, where cuBLAS alone reaches 1.38; at 1,252 tokens 0.47 and
+// 0.95 ms; 32 tokens of d 256, width 512: 5.8 us on the GPU.
 // Everything outside a tensor is read as zero by the tensor copies (ragged M, N and K) and
 // never stored.
 //
