@@ -405,6 +405,8 @@ sol_status sol_adamw_grad_norm(float* out, const sol_adamw_plan* plan, float max
     CHECK(aligned(workspace, 16), SOL_ERR_MISALIGNED, "workspace is not 16-byte aligned");
     CHECK(workspace_bytes >= SOL_ADAMW_NORM_WORKSPACE, SOL_ERR_INVALID_ARGUMENT,
           "workspace of %zu bytes is below the %d needed", workspace_bytes, SOL_ADAMW_NORM_WORKSPACE);
+    CHECK(!meet({"out", out, 1, 0, 2, 4}, {"workspace", workspace, 1, 0, SOL_ADAMW_NORM_WORKSPACE, 1}),
+          SOL_ERR_INVALID_ARGUMENT, "out overlaps workspace");
     TRY(check_plan(plan));
     return cuda_status(
         sol::launch_adamw_grad_norm(out, plan->table, plan->grad_dt, max_norm, workspace, (cudaStream_t)stream),

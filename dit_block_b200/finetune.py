@@ -58,7 +58,8 @@ class FeedForward:
         return train.ffn(y, x, *self.weights, workspace=self.workspace)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """y for x [n, d], n <= max_tokens; keeps x and the pre-activation for backward."""
+        """y for x [n, d], n <= max_tokens; keeps x and the pre-activation for backward.  y lies in this object's
+        buffer, which the next call writes."""
         n = x.shape[0]
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens are more than max_tokens ({self.max_tokens})")
@@ -66,7 +67,7 @@ class FeedForward:
         return train.ffn(self.y[:n], x, *self.weights, u=self.u[:n], workspace=self.workspace)
 
     def backward(self, dy: torch.Tensor, accumulate: bool = False) -> torch.Tensor:
-        """dx of the last forward's tokens; the weight gradients are set, or with accumulate added to."""
+        """dx (in this object's buffer) of the last forward's tokens; the weight gradients are set, or with accumulate added to."""
         if self._x is None:
             raise RuntimeError("backward needs a forward before it")
         n = self._x.shape[0]
@@ -86,7 +87,7 @@ class FeedForward:
         may change between replays.  Nothing runs now.  The graph uses this object's buffers: replays must not
         overlap its other calls, and it must not outlive ``close``."""
         g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
+        with torch.cuda.device(self.lr.device), torch.cuda.graph(g):
             self.forward(x)
             self.backward(dy)
             self.update(max_norm)

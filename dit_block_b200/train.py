@@ -99,6 +99,8 @@ def _matrix(name: str, t, rows: int, cols: int, dtype, device: int):
 def _space(workspace, device: int):
     if workspace.get_device() != device:
         raise ValueError(f"workspace must be a CUDA tensor on device {device}, as the call's other tensors")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

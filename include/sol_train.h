@@ -4,7 +4,8 @@
  * over many tensors with moments in 32 or 8 bits).
  *
  * The conventions of sol.h hold (layout, pointers, streams, errors, aliasing: only what a
- * function lists).  Bounded waits of these kernels that give up are reported by
+ * function lists; a tensor spans from its first element to its last, and a written tensor's
+ * span must not meet another's).  Bounded waits of these kernels that give up are reported by
  * sol_device_errors in bits 16..23.
  */
 #ifndef SOL_TRAIN_H
@@ -111,7 +112,7 @@ typedef struct {
 /* A plan holds the tensors' addresses on the current device (one allocation, made here and
  * freed by destroy, neither inside a stream capture; a captured graph that uses the plan must
  * not outlive it).  `tensors` is a host
- * array, copied.  Every pointer is 16-byte aligned; no written buffer may overlap another
+ * array, copied.  Every pointer is 16-byte aligned (scales: 4); no written buffer may overlap another
  * buffer of the plan.  grad_dt: SOL_DTYPE_F32 or SOL_DTYPE_BF16, of all gradients. */
 typedef struct sol_adamw_plan sol_adamw_plan;
 sol_status sol_adamw_plan_create(sol_adamw_plan** plan, const sol_adamw_tensor* tensors, int32_t n_tensors,
@@ -123,10 +124,10 @@ sol_status sol_adamw_step(const sol_adamw_plan* plan, const sol_adamw_scalars* s
 
 /* Global norm of the plan's gradients and the factor that clips it:
  *     out[0] = sqrt(sum of g^2 over all tensors),  out[1] = min(1, max_norm / (out[0] + 1e-6))
- * (device f32 [2], 16-byte aligned; a NaN norm gives a NaN factor).  Squares are scaled, so
+ * (device f32 [2], 8-byte aligned; a NaN norm gives a NaN factor).  Squares are scaled, so
  * that no gradient of f32's range overflows or vanishes; sums are formed in fp64, in a fixed
- * order.  workspace: SOL_ADAMW_NORM_WORKSPACE bytes, 16-byte aligned; calls that may overlap
- * need one each.  max_norm > 0, finite or infinite. */
+ * order.  workspace: SOL_ADAMW_NORM_WORKSPACE bytes, 16-byte aligned, apart from out; calls that may
+ * overlap need one each.  max_norm > 0, finite or infinite. */
 #define SOL_ADAMW_NORM_WORKSPACE 16384
 sol_status sol_adamw_grad_norm(float* out, const sol_adamw_plan* plan, float max_norm, void* workspace,
                                size_t workspace_bytes, sol_stream_t stream);

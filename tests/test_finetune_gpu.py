@@ -2,6 +2,10 @@
 against the same formulas in 64 bits and against itself captured in a CUDA graph."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -147,3 +151,31 @@ def test_workspace_and_sizes_of_the_full_block():
         ff.update(1.0)
         assert all(torch.isfinite(p).all() for p in ff.params)
     ff.close()
+
+
+def test_capture_as_the_first_use_of_a_process():
+    """Nothing is set up on the side by an eager call that a capture could not do by itself."""
+    code = """
+import torch
+from dit_block_b200 import finetune, sol
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+for n in (8, 300):
+    x, dy = r(n, 256), r(n, 256)
+    up, down = r(1024, 256) / 16, r(256, 512) / 16
+    a, b = (finetune.FeedForward(up, down, n, state_bits=8) for _ in range(2))
+    a.lr.fill_(1e-3); b.lr.fill_(1e-3)
+    graph = a.capture(x, dy, 1.0)
+    graph.replay()
+    b.forward(x); b.backward(dy); b.update(1.0)
+    torch.cuda.synchronize()
+    for s, t in zip([a.y, a.dx, *a.grads, *a.params], [b.y, b.dx, *b.grads, *b.params]):
+        assert torch.equal(s, t)
+    del graph
+    a.close(); b.close()
+assert sol.device_errors() == 0
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr

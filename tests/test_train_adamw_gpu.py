@@ -348,6 +348,53 @@ def test_decode_types_and_ends():
             assert (flat[0, n:] == 3).all() and (v[n:] == 3).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_past_32_bits(bits):
+    """A tensor of more than 2^32 values, zero but for its two ends, which step as tensors of their own do."""
+    ends, gap = 5000, 1 << 32
+    n = gap + ends
+    g = torch.randn(ends, device="cuda", generator=gen(1)).to(BF)
+    t = dict(params=[torch.zeros(n, device="cuda")], grads=[torch.zeros(n, device="cuda", dtype=BF)])
+    if bits == 32:
+        t["m"], t["v"] = [torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")]
+    else:
+        t["m"], t["v"] = [torch.zeros(n, device="cuda", dtype=torch.int8)], [torch.zeros(n, device="cuda", dtype=torch.uint8)]
+        blocks = -(-n // train.BLOCK)
+        t["m_scales"], t["v_scales"] = [torch.zeros(blocks, device="cuda")], [torch.zeros(blocks, device="cuda")]
+    t["grads"][0][:ends] = g
+    t["grads"][0][gap:] = g
+    out = torch.zeros(2, device="cuda")
+    with train.AdamW(**t) as opt:
+        opt.grad_norm(out, float("inf"), workspace=opt.norm_workspace())
+        opt.step(step=1, **HYPER)
+    assert abs(out[0].item() / (2 ** 0.5 * g.to(F64).norm().item()) - 1) < 1e-6
+    zero = torch.zeros(ends, device="cuda")
+    want = formula(zero, g, zero, zero, 0.0, 1, **HYPER)
+    p = t["params"][0]
+    check(p[:ends], want[0], "first values")
+    assert torch.equal(p[gap:], p[:ends])
+    assert p[ends:gap].abs().max() == 0
+    if bits == 32:
+        for k, w in (("m", want[1]), ("v", want[2])):
+            check(t[k][0][gap:], w, k)
+            assert t[k][0][ends:gap].abs().max() == 0
+    else:
+        m, v = torch.empty(n, device="cuda", dtype=BF), torch.empty(n, device="cuda", dtype=BF)
+        train.adamw_state_decode(m, v, t["m"][0], t["v"][0], t["m_scales"][0], t["v_scales"][0])
+        assert m[ends:gap].abs().max() == 0 and v[ends:gap].abs().max() == 0
+        # the ends' own blocks, read by themselves
+        at = gap // train.BLOCK
+        mt, vt = torch.empty(ends, device="cuda", dtype=BF), torch.empty(ends, device="cuda", dtype=BF)
+        train.adamw_state_decode(mt, vt, t["m"][0][gap:], t["v"][0][gap:], t["m_scales"][0][at:], t["v_scales"][0][at:])
+        assert torch.equal(m[gap:], mt) and torch.equal(v[gap:], vt)
+        # one of the table's two neighbours is within a step of it: 2 / 127 and 4 / 255 of the block's largest
+        (bm, _), (bv, _) = want[1], want[2]
+        assert ((mt.to(F64) - bm).abs() <= (2 / 127 + 2 ** -8) * bm.abs().max()).all()
+        assert ((vt.to(F64) - bv).abs() <= (4 / 255 + 2 ** -8) * bv.max()).all()
+    del t, p
+    torch.cuda.empty_cache()
+
+
 def test_refusals_on_the_device():
     t = tensors([100, 200])
     with pytest.raises(sol.SolError, match="overlaps"):

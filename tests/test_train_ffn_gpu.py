@@ -310,6 +310,36 @@ def test_captured_and_replayed():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n,ld", [(16, (1 << 28) + (1 << 26)), (300, 1 << 24)])
+def test_offsets_past_32_bits(n, ld):
+    """Rows so far apart that elements lie more than 2^32 from the first: the bits of the same call on packed
+    tensors."""
+    d, inner = 72, 136
+
+    def far(t, rows_apart=ld):
+        out = torch.empty((t.shape[0], rows_apart), device="cuda", dtype=t.dtype)[:, :t.shape[1]]
+        assert (out.shape[0] - 1) * rows_apart > 1 << 32
+        return out.copy_(t)
+
+    i = inputs(n, d, inner)
+    dy = drawn(4, n, d, 0.1)
+    ws = train.ffn_workspace(n, d, inner)
+    y, u = torch.empty((n, d), device="cuda", dtype=BF), torch.empty((n, 2 * inner), device="cuda", dtype=BF)
+    want = grads(n, d, inner, F32)
+    train.ffn(y, i["x"], i["w_up"], i["w_down"], u=u, workspace=ws)
+    train.ffn_backward(dy, i["x"], u, i["w_up"], i["w_down"], workspace=ws, **want)
+    x, w_up, fy, fu = far(i["x"]), far(i["w_up"], 1 << 24), far(torch.zeros_like(y)), far(torch.zeros_like(u))
+    train.ffn(fy, x, w_up, i["w_down"], u=fu, workspace=ws)
+    assert torch.equal(fy, y) and torch.equal(fu, u)
+    del fy
+    got = {**grads(n, d, inner, F32), "dx": far(torch.zeros_like(y)), "dw_up": far(torch.zeros_like(want["dw_up"]), 1 << 24)}
+    train.ffn_backward(far(dy), x, fu, w_up, i["w_down"], workspace=ws, **got)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    del x, w_up, fu, got
+    torch.cuda.empty_cache()
+
+
 def test_refused_sizes():
     i = inputs(4, 64, 128)
     with pytest.raises(sol.SolError, match="below the"):

@@ -187,7 +187,8 @@ def test_grad_norm_and_decode_refusals(L):
         assert L.sol_adamw_grad_norm(FAKE, None, bad, FAKE, n, None) == INV
         assert "max_norm" in last(L)
     assert L.sol_adamw_grad_norm(FAKE, None, 1.0, FAKE, n - 1, None) == INV
-    assert L.sol_adamw_grad_norm(FAKE, None, 1.0, FAKE, n, None) == INV and "plan is NULL" in last(L)
+    assert L.sol_adamw_grad_norm(FAKE + STEP, None, 1.0, FAKE, n, None) == INV and "plan is NULL" in last(L)
+    assert L.sol_adamw_grad_norm(FAKE + n - 8, None, 1.0, FAKE, n, None) == INV and "out overlaps" in last(L)
     d = L.sol_adamw_state_decode
     q, s = FAKE + STEP, FAKE + 2 * STEP
     assert d(FAKE, None, 2, q, None, s, None, 100, None) == UNS
@@ -233,3 +234,11 @@ def test_binding_refuses_cpu_tensors_shapes_and_types():
         train._flat("grad", torch.zeros(16)[::2], 8, torch.float32, -1)
     with pytest.raises(TypeError, match="m must be"):
         train._flat("m", torch.zeros(8), 8, torch.int8, -1)
+
+
+def test_a_workspace_is_taken_by_its_bytes():
+    """One value expanded to many is no workspace, whatever its shape says."""
+    one = torch.empty(1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="contiguous"):
+        train._space(one.expand(1 << 20), -1)
+    assert train._space(torch.empty(5, dtype=torch.float32), -1)[1] == 20
