@@ -337,7 +337,8 @@ try {
     sol_adamw_plan* r = new sol_adamw_plan{};
     r->grad_dt = grad_dt;
     r->state_bits = state_bits;
-    const size_t at = up256(rows.size() * sizeof(sol::AdamwTensor)), total = at + chunks.size() * sizeof(sol::AdamwChunk);
+    const size_t at = up256(rows.size() * sizeof(sol::AdamwTensor)), count = up256(at + chunks.size() * sizeof(sol::AdamwChunk)),
+                 total = count + sizeof(sol::AdamwCount);
     cudaError_t e = cudaGetDevice(&r->device);
     if (e == cudaSuccess && !rows.empty()) {
         e = cudaMalloc(&r->dev, total);
@@ -355,7 +356,8 @@ try {
         return cuda_status(e, "sol_adamw_plan_create");
     }
     r->table = {static_cast<const sol::AdamwTensor*>(r->dev),
-                reinterpret_cast<const sol::AdamwChunk*>((const char*)r->dev + at), (int64_t)chunks.size()};
+                reinterpret_cast<const sol::AdamwChunk*>((const char*)r->dev + at), (int64_t)chunks.size(),
+                reinterpret_cast<sol::AdamwCount*>((char*)r->dev + count)};
     *plan = r;
     return SOL_OK;
 } catch (const std::bad_alloc&) {

@@ -87,10 +87,15 @@ struct AdamwChunk {
     int32_t tensor;
     int32_t index;     // chunk inside the tensor
 };
+struct AdamwCount {  // of a step counted on the device
+    float inv_bc1, inv_bc2;
+    uint32_t step;
+};
 struct AdamwTable {
     const AdamwTensor* tensors;
     const AdamwChunk* chunks;
     int64_t n_chunks;
+    AdamwCount* count;  // the steps of a plan run one after another
 };
 
 cudaError_t launch_adamw_step(const AdamwTable& t, sol_dtype grad_dt, int state_bits, const sol_adamw_scalars& h,

@@ -119,7 +119,8 @@ sol_status sol_adamw_plan_create(sol_adamw_plan** plan, const sol_adamw_tensor* 
                                  sol_dtype grad_dt, int32_t state_bits);
 sol_status sol_adamw_plan_destroy(sol_adamw_plan* plan);
 
-/* One step over all tensors of the plan: one kernel.  Two steps of one plan must not overlap. */
+/* One step over all tensors of the plan: one kernel, and with step_device and many values a small one
+ * ahead of it.  Two steps of one plan must not overlap. */
 sol_status sol_adamw_step(const sol_adamw_plan* plan, const sol_adamw_scalars* scalars, sol_stream_t stream);
 
 /* Global norm of the plan's gradients and the factor that clips it:

@@ -127,9 +127,9 @@ def test_a_zero_gradient_and_zero_moments():
     assert torch.equal(p, before)
 
 
-def test_scalars_from_the_device_in_a_captured_step():
+@pytest.mark.parametrize("sizes", [[1000, 5000], [70, 2_000_000]])
+def test_scalars_from_the_device_in_a_captured_step(sizes):
     """lr, step and the clip factor are read when the graph runs; the host's lr and step are not used."""
-    sizes = [1000, 5000]
     t, ref = tensors(sizes), tensors(sizes)
     lr = torch.tensor([5e-4], device="cuda")
     step = torch.tensor([1], device="cuda")
