@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -34,6 +35,10 @@ class AdamwScalars(ctypes.Structure):
                 ("lr_device", _P), ("step_device", _P), ("grad_factor", _P)]
 
 
+_pack_scalars = struct.Struct("4dqQ3P").pack  # an AdamwScalars in a third of the time
+assert struct.calcsize("4dqQ3P") == ctypes.sizeof(AdamwScalars)
+
+
 SIGNATURES = {
     "sol_ffn_workspace_bytes": ([_I64, _I64, _I64], _SZ),
     "sol_ffn": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _I64, _I64, _I64, _E, _P], _E),
@@ -41,7 +46,7 @@ SIGNATURES = {
                           _P, _SZ, _I64, _I64, _I64, _E, _P], _E),
     "sol_adamw_plan_create": ([ctypes.POINTER(_P), ctypes.POINTER(AdamwTensor), _I32, _E, _I32], _E),
     "sol_adamw_plan_destroy": ([_P], _E),
-    "sol_adamw_step": ([_P, ctypes.POINTER(AdamwScalars), _P], _E),
+    "sol_adamw_step": ([_P, _P, _P], _E),  # plan, sol_adamw_scalars, stream
     "sol_adamw_grad_norm": ([_P, _P, _F, _P, _SZ, _P], _E),
     "sol_adamw_state_decode": ([_P, _P, _E, _P, _P, _P, _P, _I64, _P], _E),
 }
@@ -66,7 +71,7 @@ def _call(name: str, device: int, stream, *args):
     """Calls a function whose last argument is the stream, with `device` the current one."""
     fn = getattr(_lib or lib(), name)
     stream = torch._C._cuda_getCurrentRawStream(device) if stream is None else sol._stream(stream)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -77,13 +82,16 @@ def _call(name: str, device: int, stream, *args):
 
 def _device(t) -> int:
     """The index of the CUDA device that a call's first tensor lies on; the others must lie there too."""
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0 or not t.is_cuda:
         raise ValueError("libsol takes CUDA tensors")
-    return t.get_device()
+    return device
 
 
 def _matrix(name: str, t, rows: int, cols: int, dtype, device: int):
     """(address, row stride) of a [rows, cols] argument; a single row may have any stride."""
+    if t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr(), cols
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     if t.dtype is not dtype:
@@ -101,7 +109,7 @@ def _space(workspace, device: int):
         raise ValueError(f"workspace must be a CUDA tensor on device {device}, as the call's other tensors")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 _NONE = (None, 0)
@@ -217,11 +225,11 @@ class AdamW:
         """One step (sol_adamw_step).  lr_device (f32) and step_device (int64) are device scalars read in place
         of lr and step when the step runs; grad_factor (f32) multiplies the gradients."""
         dev = self._index
-        h = AdamwScalars(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFFFFFFFFFF,
-                         None if lr_device is None else _flat("lr_device", lr_device, 1, torch.float32, dev),
-                         None if step_device is None else _flat("step_device", step_device, 1, torch.int64, dev),
-                         None if grad_factor is None else _flat("grad_factor", grad_factor, 1, torch.float32, dev))
-        _call("sol_adamw_step", dev, stream, self._handle, ctypes.byref(h))
+        h = _pack_scalars(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFFFFFFFFFF,
+                          0 if lr_device is None else _flat("lr_device", lr_device, 1, torch.float32, dev),
+                          0 if step_device is None else _flat("step_device", step_device, 1, torch.int64, dev),
+                          0 if grad_factor is None else _flat("grad_factor", grad_factor, 1, torch.float32, dev))
+        _call("sol_adamw_step", dev, stream, self._handle, h)
 
     def norm_workspace(self) -> torch.Tensor:
         """A workspace for grad_norm (one for each of the calls that may overlap)."""
