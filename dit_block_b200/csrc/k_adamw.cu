@@ -20,9 +20,10 @@ namespace sol {
 namespace adamw {
 
 constexpr int THREADS = 256;
-constexpr int BLOCK = SOL_ADAMW_BLOCK;
+constexpr int BLOCK = SOL_ADAMW_BLOCK, HALF = BLOCK / 2;
 constexpr int CHUNK = kAdamwChunk;
-constexpr int STEP8_CTAS = 3;         // 80 registers: no spills (4 CTAs of 64 registers: 1077 against 1060 us)
+constexpr int STEP8_THREADS = 128, STEP8_SPLIT = THREADS / STEP8_THREADS;
+constexpr int STEP8_CTAS = 3 * STEP8_SPLIT;         // 80 registers: no spills (4 CTAs of 64 registers: 1077 against 1060 us)
 constexpr int NORM_CTAS = 148 * 8;  // partial sums of the gradient norm
 static_assert((NORM_CTAS) * sizeof(double) <= SOL_ADAMW_NORM_WORKSPACE, "the norm's partial sums must fit its workspace");
 
@@ -347,19 +348,11 @@ __device__ __forceinline__ Unit unit_of(float s, float most)
     u.inv = s > 0.f ? most * rcp_ftz(s * u.pre) : 0.f;  // off by 2^-22: the margin of 2^-20 covers it
     return u;
 }
-// The codes of a lane's eight new moments and the scales of their block; values from `live` on
-// lie behind the tensor's end.
-__device__ __forceinline__ void encode8(float2* m, float2* v, uint32_t at, int live, uint2& q1, uint2& q2, float& n1,
-                                        float& n2)
+// The codes of a lane's eight new moments (two runs of four, HALF apart; `at`: the hash's argument for the
+// first) and the scales of their block.
+__device__ __forceinline__ void encode8(float2* m, float2* v, uint32_t at, uint2& q1, uint2& q2, float& n1, float& n2)
 {
     float top1 = 0.f, top2 = 0.f;
-    if (live < 8) {  // values past the tensor's end count for nothing
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (2 * e >= live) m[e].x = v[e].x = 0.f;
-            if (2 * e + 1 >= live) m[e].y = v[e].y = 0.f;
-        }
-    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         top1 = max_abs_nan(top1, m[e].x, m[e].y);
@@ -375,7 +368,7 @@ __device__ __forceinline__ void encode8(float2* m, float2* v, uint32_t at, int l
         float2 z[4], up[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const uint32_t r0 = mixed(at + 4 * w + 2 * e), r1 = mixed(at + 4 * w + 2 * e + 1);
+            const uint32_t r0 = mixed(at + HALF * w + 2 * e), r1 = mixed(at + HALF * w + 2 * e + 1);
             encode_first2(m[2 * w + e], u1.inv, r0, r1, z[e], up[e]);
             encode_second2(v[2 * w + e], u2.inv, r0, r1, z[2 + e], up[2 + e]);
         }
@@ -384,32 +377,41 @@ __device__ __forceinline__ void encode8(float2* m, float2* v, uint32_t at, int l
     }
 }
 
-// A lane's part of a block on its way through shared memory: every lane copies and reads its own
-// eight values only, so that no barrier is needed, and the next block's loads are in flight
-// while a block is worked on, without registers for them.
-template <typename G> struct alignas(16) LaneIn {
-    float p[8];
-    G g[8];
-    uint2 m, v;
+// A block on its way through shared memory: the next one's loads are in flight while a block is
+// worked on, without registers for them.  A lane takes values [4 * lane, + 4) of either half, so that
+// every load and store of a warp is one run of bytes.
+template <typename G> struct alignas(16) BlockIn {
+    float p[BLOCK];
+    G g[BLOCK];
+    uint8_t mv[2][BLOCK];
 };
 
 __device__ __forceinline__ void copy16(void* dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy8(void* dst, const void* src)
+__device__ __forceinline__ void load4s(const float* p, float2* f)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    unpack2<float>(*reinterpret_cast<const uint4*>(p), f);
+}
+__device__ __forceinline__ void load4s(const bf16* p, float2* f)
+{
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    f[0] = make_float2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+    f[1] = make_float2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
 
-// A warp takes one block of 256 values at a time, eight a lane, two blocks in flight.
+// A warp takes one block of 256 values at a time, eight a lane, two blocks in flight.  A CTA is small
+// so that its warps need not wait for each other's end, and is done after two blocks a warp, so that reads and
+// writes stay close together in memory (212 M values, bf16 gradients and copies: CTAs of 256 threads 718 us, of
+// 128 679; with four blocks a warp 984).
 template <typename G, bool ROOT_FTZ>
-__global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable t, const __grid_constant__ Scalars h)
+__global__ void __launch_bounds__(STEP8_THREADS, STEP8_CTAS) k_step8(const AdamwTable t, const __grid_constant__ Scalars h)
 {
-    __shared__ LaneIn<G> in[2][THREADS];
-    const AdamwChunk c = t.chunks[blockIdx.x];
+    __shared__ BlockIn<G> in[2][STEP8_THREADS / 32];
+    const AdamwChunk c = t.chunks[blockIdx.x / STEP8_SPLIT];
     const AdamwTensor x = t.tensors[c.tensor];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = blockIdx.x % STEP8_SPLIT * (STEP8_THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const G* grad = static_cast<const G*>(x.g);
     uint8_t *pm = static_cast<uint8_t*>(x.m), *pv = static_cast<uint8_t*>(x.v);
     bf16* copy = static_cast<bf16*>(x.copy);
@@ -419,14 +421,13 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
 
     auto fetch = [&](int64_t from, int stage) {  // whole blocks only
         if (from + BLOCK <= end) {
-            LaneIn<G>& d = in[stage][threadIdx.x];
-            const int64_t i = from + 8 * lane;
-            copy16(d.p, x.p + i);
-            copy16(d.p + 4, x.p + i + 4);
-            copy16(d.g, grad + i);
-            if (sizeof(G) == 4) copy16(d.g + 4, grad + i + 4);
-            copy8(&d.m, pm + i);
-            copy8(&d.v, pv + i);
+            BlockIn<G>& d = in[stage][threadIdx.x >> 5];
+            constexpr int V = 16 / sizeof(G);
+            copy16(d.p + 4 * lane, x.p + from + 4 * lane);
+            copy16(d.p + HALF + 4 * lane, x.p + from + HALF + 4 * lane);
+#pragma unroll
+            for (int e = 0; e < BLOCK; e += 32 * V) copy16(d.g + e + V * lane, grad + from + e + V * lane);
+            copy16(&d.mv[0][16 * lane], (lane < 16 ? pm : pv) + from + 16 * (lane & 15));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
     const uint32_t from = mixed(key + (uint32_t)((uint64_t)c.index * CHUNK >> 32));  // a chunk's upper halves agree
     for (int stage = 0; start < end; start += STRIDE, stage ^= 1) {
         fetch(start + STRIDE, stage ^ 1);
-        const int64_t blk = start / BLOCK, i = start + 8 * lane;
+        const int64_t blk = start / BLOCK, i = start + 4 * lane;
         float n1 = s1, n2 = s2;
         if (start + STRIDE < end) {
             s1 = x.ms[blk + THREADS / 32];
@@ -452,32 +453,47 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
         uint2 q1, q2;
         if (start + BLOCK <= end) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            const LaneIn<G>& d = in[stage][threadIdx.x];
-            unpack2<float>(*reinterpret_cast<const uint4*>(d.p), p);
-            unpack2<float>(*reinterpret_cast<const uint4*>(d.p + 4), p + 2);
-            unpack2<G>(*reinterpret_cast<const uint4*>(d.g), g);
-            if (sizeof(G) == 4) unpack2<G>(*reinterpret_cast<const uint4*>(d.g + 4), g + 2);
-            decode_first8(d.m, n1, m);
-            decode_second8(d.v, n2, v);
+            __syncwarp();
+            const BlockIn<G>& d = in[stage][threadIdx.x >> 5];
+            uint32_t w[2][2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                load4s(d.p + r * HALF + 4 * lane, p + 2 * r);
+                load4s(d.g + r * HALF + 4 * lane, g + 2 * r);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) w[k][r] = *reinterpret_cast<const uint32_t*>(&d.mv[k][r * HALF + 4 * lane]);
+            }
+            __syncwarp();  // read before the next block but one is copied here
+            decode_first8(make_uint2(w[0][0], w[0][1]), n1, m);
+            decode_second8(make_uint2(w[1][0], w[1][1]), n2, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) update2<ROOT_FTZ>(p[e], m[e], v[e], g[e], -l.lr * l.inv_bc1, -l.lr * x.wd, h, l);
             // the parameters leave first: their registers are free for the codes
             st_stream(x.p + i, pack2<float>(p));
-            st_stream(x.p + i + 4, pack2<float>(p + 2));
-            if (copy) st_stream(copy + i, pack2<bf16>(p));
-            encode8(m, v, at, 8, q1, q2, n1, n2);
-            *reinterpret_cast<uint2*>(pm + i) = q1;
-            *reinterpret_cast<uint2*>(pv + i) = q2;
+            st_stream(x.p + i + HALF, pack2<float>(p + 2));
+            if (copy) {
+                const uint4 r = pack2<bf16>(p);
+                __stcs(reinterpret_cast<uint2*>(copy + i), make_uint2(r.x, r.y));
+                __stcs(reinterpret_cast<uint2*>(copy + i + HALF), make_uint2(r.z, r.w));
+            }
+            encode8(m, v, at, q1, q2, n1, n2);
+            *reinterpret_cast<uint32_t*>(pm + i) = q1.x;
+            *reinterpret_cast<uint32_t*>(pm + i + HALF) = q1.y;
+            *reinterpret_cast<uint32_t*>(pv + i) = q2.x;
+            *reinterpret_cast<uint32_t*>(pv + i + HALF) = q2.y;
         } else {
-            // the tensor's last block
-            const int live = (int)min((int64_t)8, max((int64_t)0, x.n - i));
+            // the tensor's last block: value e of the lane is i + e, or i + HALF + e - 4 from e = 4 on
+            const auto index = [&](int e) { return i + e + (e < 4 ? 0 : HALF - 4); };
             float fp[8] = {}, fg[8] = {};
             uint32_t w1[2] = {}, w2[2] = {};
-            for (int e = 0; e < live; ++e) {
-                fp[e] = x.p[i + e];
-                fg[e] = widen(grad[i + e]);
-                w1[e >> 2] |= (uint32_t)pm[i + e] << (8 * (e & 3));
-                w2[e >> 2] |= (uint32_t)pv[i + e] << (8 * (e & 3));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t j = index(e);
+                if (j >= x.n) continue;
+                fp[e] = x.p[j];
+                fg[e] = widen(grad[j]);
+                w1[e >> 2] |= (uint32_t)pm[j] << (8 * (e & 3));
+                w2[e >> 2] |= (uint32_t)pv[j] << (8 * (e & 3));
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -488,16 +504,20 @@ __global__ void __launch_bounds__(THREADS, STEP8_CTAS) k_step8(const AdamwTable 
             decode_second8(make_uint2(w2[0], w2[1]), n2, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) update2<ROOT_FTZ>(p[e], m[e], v[e], g[e], -l.lr * l.inv_bc1, -l.lr * x.wd, h, l);
-            encode8(m, v, at, live, q1, q2, n1, n2);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < live) {
-                    const float pe = e & 1 ? p[e / 2].y : p[e / 2].x;
-                    x.p[i + e] = pe;
-                    pm[i + e] = (uint8_t)((e < 4 ? q1.x : q1.y) >> (8 * (e & 3)));
-                    pv[i + e] = (uint8_t)((e < 4 ? q2.x : q2.y) >> (8 * (e & 3)));
-                    if (copy) copy[i + e] = __float2bfloat16_rn(pe);
-                }
+            for (int e = 0; e < 8; ++e)  // values past the tensor's end count for nothing
+                if (index(e) >= x.n) (e & 1 ? m[e / 2].y : m[e / 2].x) = (e & 1 ? v[e / 2].y : v[e / 2].x) = 0.f;
+            encode8(m, v, at, q1, q2, n1, n2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t j = index(e);
+                if (j >= x.n) continue;
+                const float pe = e & 1 ? p[e / 2].y : p[e / 2].x;
+                x.p[j] = pe;
+                pm[j] = (uint8_t)((e < 4 ? q1.x : q1.y) >> (8 * (e & 3)));
+                pv[j] = (uint8_t)((e < 4 ? q2.x : q2.y) >> (8 * (e & 3)));
+                if (copy) copy[j] = __float2bfloat16_rn(pe);
+            }
         }
         if (lane == 0) {
             x.ms[blk] = n1;
@@ -668,7 +688,7 @@ cudaError_t launch_adamw_step(const AdamwTable& t, sol_dtype grad_dt, int state_
     // The powers of a step counted on the device: in each CTA where all run at once, which costs 1 us and the
     // launch of k_count 5 (20,000 values, 8 bits: 7.9 against 13.2 us a call); else k_count, once for all (212 M
     // values: 733 against 863 us, 720 with the host's step).
-    const bool counted = a.step_device && t.n_chunks > 148 * adamw::STEP8_CTAS;
+    const bool counted = a.step_device && t.n_chunks > 148 * 3;
     if (counted) {
         h.count = t.count;
         adamw::k_count<<<1, 64, 0, s>>>(h, t.count);
@@ -684,8 +704,9 @@ cudaError_t launch_adamw_step(const AdamwTable& t, sol_dtype grad_dt, int state_
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     la[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)t.n_chunks);
-    cfg.blockDim = dim3(adamw::THREADS);
+    const int split = state_bits == 32 ? 1 : adamw::STEP8_SPLIT;
+    cfg.gridDim = dim3((unsigned)(t.n_chunks * split));
+    cfg.blockDim = dim3(adamw::THREADS / split);
     cfg.stream = s;
     cfg.attrs = la;
     cfg.numAttrs = counted ? 1 : 0;  // behind k_count alone
