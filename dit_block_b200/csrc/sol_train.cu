@@ -167,102 +167,101 @@ size_t sol_ffn_workspace_bytes(int64_t n_tokens, int64_t d, int64_t inner)
     return std::max<size_t>(ffn_layout(n_tokens, d, inner).total, 256);
 }
 
-sol_status sol_ffn(void* y, int64_t ld_y, void* u, int64_t ld_u, const void* x, int64_t ld_x, const void* w_up,
-                   int64_t ld_wu, const void* w_down, int64_t ld_wd, void* workspace, size_t workspace_bytes,
-                   int64_t n_tokens, int64_t d, int64_t inner, sol_dtype dt, sol_stream_t stream)
+sol_status sol_ffn(const sol_ffn_desc* desc, sol_stream_t stream)
 {
-    TRY(check_ffn_sizes(n_tokens, d, inner, dt));
-    const int64_t T = n_tokens;
-    const Span sw[2] = {{"w_up", w_up, 2 * inner, ld_wu, d, 2}, {"w_down", w_down, d, ld_wd, inner, 2}};
+    CHECK(desc, SOL_ERR_INVALID_ARGUMENT, "desc is NULL");
+    const sol_ffn_desc& f = *desc;
+    const int64_t T = f.n_tokens, d = f.d, inner = f.inner;
+    TRY(check_ffn_sizes(T, d, inner, f.dt));
+    const Span sw[2] = {{"w_up", f.w_up, 2 * inner, f.ld_wu, d, 2}, {"w_down", f.w_down, d, f.ld_wd, inner, 2}};
     TRY(check_rows(sw[0]));
     TRY(check_rows(sw[1]));
     if (T == 0) return SOL_OK;
     const FfnWorkspace lay = ffn_layout(T, d, inner);
-    TRY(check_workspace(workspace, workspace_bytes, lay));
-    const Span written[3] = {{"y", y, T, ld_y, d, 2}, {"u", u, T, ld_u, 2 * inner, 2},
-                             {"workspace", workspace, 1, 0, (int64_t)lay.total, 1}};
-    const Span read[3] = {sw[0], sw[1], {"x", x, T, ld_x, d, 2}};
+    TRY(check_workspace(f.workspace, f.workspace_bytes, lay));
+    const Span written[3] = {{"y", f.y, T, f.ld_y, d, 2}, {"u", f.u, T, f.ld_u, 2 * inner, 2},
+                             {"workspace", f.workspace, 1, 0, (int64_t)lay.total, 1}};
+    const Span read[3] = {sw[0], sw[1], {"x", f.x, T, f.ld_x, d, 2}};
     TRY(check_rows(written[0]));
-    if (u) TRY(check_rows(written[1]));
+    if (f.u) TRY(check_rows(written[1]));
     TRY(check_rows(read[2]));
     TRY(check_apart(written, 3, read, 3));
     const cudaStream_t s = (cudaStream_t)stream;
-    void* act = (char*)workspace + lay.act;
+    void* act = (char*)f.workspace + lay.act;
     if (sol::ffn_small_fits(T, d, inner)) {
-        const sol::FfnSmall f{(int32_t)T, (int32_t)d, (int32_t)inner, x, w_up, w_down, ld_x, ld_wu, ld_wd, y, u, act, ld_y, ld_u};
-        return cuda_status(sol::launch_ffn_small(f, s), "sol_ffn launch");
+        const sol::FfnSmall small{(int32_t)T, (int32_t)d, (int32_t)inner, f.x, f.w_up, f.w_down, f.ld_x, f.ld_wu, f.ld_wd,
+                                  f.y, f.u, act, f.ld_y, f.ld_u};
+        return cuda_status(sol::launch_ffn_small(small, s), "sol_ffn launch");
     }
-    sol::FfnProduct g = product(sol::FFN_UP, T, inner, d, {x, T, d, ld_x}, false, {w_up, 2 * inner, d, ld_wu}, false,
-                                act, inner, workspace, lay);
-    g.u = u;
-    g.ld_u = ld_u;
+    sol::FfnProduct g = product(sol::FFN_UP, T, inner, d, {f.x, T, d, f.ld_x}, false, {f.w_up, 2 * inner, d, f.ld_wu}, false,
+                                act, inner, f.workspace, lay);
+    g.u = f.u;
+    g.ld_u = f.ld_u;
     TRY(cuda_status(sol::launch_ffn_products(&g, 1, false, s), "sol_ffn up projection launch"));
-    g = product(sol::FFN_STORE, T, d, inner, {act, T, inner, inner}, false, {w_down, d, inner, ld_wd}, false, y, ld_y,
-                workspace, lay);
+    g = product(sol::FFN_STORE, T, d, inner, {act, T, inner, inner}, false, {f.w_down, d, inner, f.ld_wd}, false, f.y, f.ld_y,
+                f.workspace, lay);
     return cuda_status(sol::launch_ffn_products(&g, 1, true, s), "sol_ffn down projection launch");
 }
 
-sol_status sol_ffn_backward(void* dx, int64_t ld_dx, void* dw_up, int64_t ld_dwu, void* dw_down, int64_t ld_dwd,
-                            sol_dtype grad_dt, int32_t accumulate, const void* dy, int64_t ld_dy, const void* x,
-                            int64_t ld_x, const void* u, int64_t ld_u, const void* w_up, int64_t ld_wu,
-                            const void* w_down, int64_t ld_wd, void* workspace, size_t workspace_bytes,
-                            int64_t n_tokens, int64_t d, int64_t inner, sol_dtype dt, sol_stream_t stream)
+sol_status sol_ffn_backward(const sol_ffn_backward_desc* desc, sol_stream_t stream)
 {
-    TRY(check_ffn_sizes(n_tokens, d, inner, dt));
-    CHECK(grad_dt == SOL_DTYPE_F32 || grad_dt == SOL_DTYPE_BF16, SOL_ERR_UNSUPPORTED,
-          "grad_dt %d is not SOL_DTYPE_F32 or SOL_DTYPE_BF16", (int)grad_dt);
-    const int64_t T = n_tokens;
-    const size_t ge = grad_dt == SOL_DTYPE_F32 ? 4 : 2;
+    CHECK(desc, SOL_ERR_INVALID_ARGUMENT, "desc is NULL");
+    const sol_ffn_backward_desc& f = *desc;
+    const int64_t T = f.n_tokens, d = f.d, inner = f.inner;
+    TRY(check_ffn_sizes(T, d, inner, f.dt));
+    CHECK(f.grad_dt == SOL_DTYPE_F32 || f.grad_dt == SOL_DTYPE_BF16, SOL_ERR_UNSUPPORTED,
+          "grad_dt %d is not SOL_DTYPE_F32 or SOL_DTYPE_BF16", (int)f.grad_dt);
+    const size_t ge = f.grad_dt == SOL_DTYPE_F32 ? 4 : 2;
     const cudaStream_t s = (cudaStream_t)stream;
     const FfnWorkspace lay = ffn_layout(T, d, inner);
-    const Span written[4] = {{"dw_up", dw_up, 2 * inner, ld_dwu, d, ge}, {"dw_down", dw_down, d, ld_dwd, inner, ge},
-                             {"dx", T ? dx : nullptr, T, ld_dx, d, 2},
-                             {"workspace", T ? workspace : nullptr, 1, 0, (int64_t)lay.total, 1}};
-    const Span read[5] = {{"dy", dy, T, ld_dy, d, 2}, {"u", u, T, ld_u, 2 * inner, 2}, {"x", x, T, ld_x, d, 2},
-                          {"w_up", w_up, 2 * inner, ld_wu, d, 2}, {"w_down", w_down, d, ld_wd, inner, 2}};
+    const Span written[4] = {{"dw_up", f.dw_up, 2 * inner, f.ld_dwu, d, ge}, {"dw_down", f.dw_down, d, f.ld_dwd, inner, ge},
+                             {"dx", T ? f.dx : nullptr, T, f.ld_dx, d, 2},
+                             {"workspace", T ? f.workspace : nullptr, 1, 0, (int64_t)lay.total, 1}};
+    const Span read[5] = {{"dy", f.dy, T, f.ld_dy, d, 2}, {"u", f.u, T, f.ld_u, 2 * inner, 2}, {"x", f.x, T, f.ld_x, d, 2},
+                          {"w_up", f.w_up, 2 * inner, f.ld_wu, d, 2}, {"w_down", f.w_down, d, f.ld_wd, inner, 2}};
     for (int i = 0; i < 3; ++i)
         if (written[i].p) TRY(check_rows(written[i]));
     TRY(check_rows(read[3]));
     TRY(check_rows(read[4]));
     if (T > 0) {
         for (int i = 0; i < 3; ++i) TRY(check_rows(read[i]));
-        TRY(check_workspace(workspace, workspace_bytes, lay));
+        TRY(check_workspace(f.workspace, f.workspace_bytes, lay));
     }
     TRY(check_apart(written, 4, read, 5));
     if (T == 0) {
         // a sum over no tokens
-        for (int i = 0; i < 2 && !accumulate; ++i)
+        for (int i = 0; i < 2 && !f.accumulate; ++i)
             if (written[i].p)
                 TRY(cuda_status(cudaMemset2DAsync(const_cast<void*>(written[i].p), (size_t)written[i].ld * ge, 0,
                                                   (size_t)written[i].width * ge, (size_t)written[i].rows, s),
                                 "sol_ffn_backward"));
         return SOL_OK;
     }
-    if (!dx && !dw_up && !dw_down) return SOL_OK;
-    void* act = (char*)workspace + lay.act;
-    void* du = (char*)workspace + lay.du;
+    if (!f.dx && !f.dw_up && !f.dw_down) return SOL_OK;
+    void* act = (char*)f.workspace + lay.act;
+    void* du = (char*)f.workspace + lay.du;
     // d_act, and in its epilogue du and act
-    sol::FfnProduct g = product(sol::FFN_DACT, T, inner, d, {dy, T, d, ld_dy}, false, {w_down, d, inner, ld_wd}, true,
-                                dw_down ? act : nullptr, inner, workspace, lay);
-    g.u = const_cast<void*>(u);
-    g.ld_u = ld_u;
+    sol::FfnProduct g = product(sol::FFN_DACT, T, inner, d, {f.dy, T, d, f.ld_dy}, false, {f.w_down, d, inner, f.ld_wd}, true,
+                                f.dw_down ? act : nullptr, inner, f.workspace, lay);
+    g.u = const_cast<void*>(f.u);
+    g.ld_u = f.ld_u;
     g.du = du;
     g.ld_du = 2 * inner;
     TRY(cuda_status(sol::launch_ffn_products(&g, 1, false, s), "sol_ffn_backward d_act launch"));
     sol::FfnProduct all[3];
     int n = 0;
-    if (dx)
-        all[n++] = product(sol::FFN_STORE, T, d, 2 * inner, {du, T, 2 * inner, 2 * inner}, false, {w_up, 2 * inner, d, ld_wu},
-                           true, dx, ld_dx, workspace, lay);
-    if (dw_up)
-        all[n++] = product(sol::FFN_STORE, 2 * inner, d, T, {du, T, 2 * inner, 2 * inner}, true, {x, T, d, ld_x}, true,
-                           dw_up, ld_dwu, workspace, lay);
-    if (dw_down)
-        all[n++] = product(sol::FFN_STORE, d, inner, T, {dy, T, d, ld_dy}, true, {act, T, inner, inner}, true, dw_down,
-                           ld_dwd, workspace, lay);
-    for (int i = dx ? 1 : 0; i < n; ++i) {
-        all[i].out_f32 = grad_dt == SOL_DTYPE_F32;
-        all[i].accumulate = accumulate != 0;
+    if (f.dx)
+        all[n++] = product(sol::FFN_STORE, T, d, 2 * inner, {du, T, 2 * inner, 2 * inner}, false, {f.w_up, 2 * inner, d, f.ld_wu},
+                           true, f.dx, f.ld_dx, f.workspace, lay);
+    if (f.dw_up)
+        all[n++] = product(sol::FFN_STORE, 2 * inner, d, T, {du, T, 2 * inner, 2 * inner}, true, {f.x, T, d, f.ld_x}, true,
+                           f.dw_up, f.ld_dwu, f.workspace, lay);
+    if (f.dw_down)
+        all[n++] = product(sol::FFN_STORE, d, inner, T, {f.dy, T, d, f.ld_dy}, true, {act, T, inner, inner}, true, f.dw_down,
+                           f.ld_dwd, f.workspace, lay);
+    for (int i = f.dx ? 1 : 0; i < n; ++i) {
+        all[i].out_f32 = f.grad_dt == SOL_DTYPE_F32;
+        all[i].accumulate = f.accumulate != 0;
     }
     return cuda_status(sol::launch_ffn_products(all, n, true, s), "sol_ffn_backward gradients launch");
 }

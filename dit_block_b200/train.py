@@ -35,15 +35,40 @@ class AdamwScalars(ctypes.Structure):
                 ("lr_device", _P), ("step_device", _P), ("grad_factor", _P)]
 
 
-_pack_scalars = struct.Struct("4dqQ3P").pack  # an AdamwScalars in a third of the time
-assert struct.calcsize("4dqQ3P") == ctypes.sizeof(AdamwScalars)
+def _rows(*names):
+    return [f for n, ld in names for f in ((n, _P), (ld, _I64))]
+
+
+class FfnDesc(ctypes.Structure):
+    """sol_ffn_desc."""
+    _fields_ = [*_rows(("y", "ld_y"), ("u", "ld_u"), ("x", "ld_x"), ("w_up", "ld_wu"), ("w_down", "ld_wd")),
+                ("workspace", _P), ("workspace_bytes", _SZ), ("n_tokens", _I64), ("d", _I64), ("inner", _I64), ("dt", _E)]
+
+
+class FfnBackwardDesc(ctypes.Structure):
+    """sol_ffn_backward_desc."""
+    _fields_ = [*_rows(("dx", "ld_dx"), ("dw_up", "ld_dwu"), ("dw_down", "ld_dwd"), ("dy", "ld_dy"), ("x", "ld_x"),
+                       ("u", "ld_u"), ("w_up", "ld_wu"), ("w_down", "ld_wd")),
+                ("workspace", _P), ("workspace_bytes", _SZ), ("n_tokens", _I64), ("d", _I64), ("inner", _I64), ("dt", _E),
+                ("grad_dt", _E), ("accumulate", _I32)]
+
+
+def _packer(form: str, of) -> struct.Struct:
+    """The bytes of a ctypes structure from its fields, in a third of the time."""
+    s = struct.Struct(form + "0q")  # with the structure's alignment at its end
+    assert s.size == ctypes.sizeof(of)
+    return s.pack
+
+
+_pack_scalars = _packer("4dqQ3P", AdamwScalars)
+_pack_ffn = _packer("PqPqPqPqPqPN3qi", FfnDesc)
+_pack_ffn_backward = _packer("PqPqPqPqPqPqPqPqPN3q3i", FfnBackwardDesc)
 
 
 SIGNATURES = {
     "sol_ffn_workspace_bytes": ([_I64, _I64, _I64], _SZ),
-    "sol_ffn": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _I64, _I64, _I64, _E, _P], _E),
-    "sol_ffn_backward": ([_P, _I64, _P, _I64, _P, _I64, _E, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
-                          _P, _SZ, _I64, _I64, _I64, _E, _P], _E),
+    "sol_ffn": ([_P, _P], _E),           # sol_ffn_desc, stream
+    "sol_ffn_backward": ([_P, _P], _E),  # sol_ffn_backward_desc, stream
     "sol_adamw_plan_create": ([ctypes.POINTER(_P), ctypes.POINTER(AdamwTensor), _I32, _E, _I32], _E),
     "sol_adamw_plan_destroy": ([_P], _E),
     "sol_adamw_step": ([_P, _P, _P], _E),  # plan, sol_adamw_scalars, stream
@@ -112,7 +137,7 @@ def _space(workspace, device: int):
     return workspace.data_ptr(), workspace.nbytes
 
 
-_NONE = (None, 0)
+_NONE = (0, 0)
 
 
 # ---------------------------------------------------------------- gated feed-forward block
@@ -137,10 +162,10 @@ def ffn(y, x, w_up, w_down, *, u=None, workspace, stream=None):
     n, d = x.shape
     inner = w_down.shape[1]
     dev = _device(x)
-    args = (*_matrix("y", y, n, d, bf, dev), *(_NONE if u is None else _matrix("u", u, n, 2 * inner, bf, dev)),
-            *_matrix("x", x, n, d, bf, dev), *_matrix("w_up", w_up, 2 * inner, d, bf, dev),
-            *_matrix("w_down", w_down, d, inner, bf, dev), *_space(workspace, dev), n, d, inner, sol.BF16)
-    _call("sol_ffn", dev, stream, *args)
+    desc = _pack_ffn(*_matrix("y", y, n, d, bf, dev), *(_NONE if u is None else _matrix("u", u, n, 2 * inner, bf, dev)),
+                     *_matrix("x", x, n, d, bf, dev), *_matrix("w_up", w_up, 2 * inner, d, bf, dev),
+                     *_matrix("w_down", w_down, d, inner, bf, dev), *_space(workspace, dev), n, d, inner, sol.BF16)
+    _call("sol_ffn", dev, stream, desc)
     return y
 
 
@@ -156,14 +181,14 @@ def ffn_backward(dy, x, u, w_up, w_down, *, dx=None, dw_up=None, dw_down=None, a
     if grad is not bf and grad is not torch.float32:
         raise TypeError(f"dw_up and dw_down must be torch.bfloat16 or torch.float32, got {grad}")
     dev = _device(x)
-    args = (*(_NONE if dx is None else _matrix("dx", dx, n, d, bf, dev)),
-            *(_NONE if dw_up is None else _matrix("dw_up", dw_up, 2 * inner, d, grad, dev)),
-            *(_NONE if dw_down is None else _matrix("dw_down", dw_down, d, inner, grad, dev)),
-            sol.BF16 if grad is bf else sol.F32, 1 if accumulate else 0, *_matrix("dy", dy, n, d, bf, dev),
-            *_matrix("x", x, n, d, bf, dev), *_matrix("u", u, n, 2 * inner, bf, dev),
-            *_matrix("w_up", w_up, 2 * inner, d, bf, dev), *_matrix("w_down", w_down, d, inner, bf, dev),
-            *_space(workspace, dev), n, d, inner, sol.BF16)
-    _call("sol_ffn_backward", dev, stream, *args)
+    desc = _pack_ffn_backward(
+        *(_NONE if dx is None else _matrix("dx", dx, n, d, bf, dev)),
+        *(_NONE if dw_up is None else _matrix("dw_up", dw_up, 2 * inner, d, grad, dev)),
+        *(_NONE if dw_down is None else _matrix("dw_down", dw_down, d, inner, grad, dev)),
+        *_matrix("dy", dy, n, d, bf, dev), *_matrix("x", x, n, d, bf, dev), *_matrix("u", u, n, 2 * inner, bf, dev),
+        *_matrix("w_up", w_up, 2 * inner, d, bf, dev), *_matrix("w_down", w_down, d, inner, bf, dev),
+        *_space(workspace, dev), n, d, inner, sol.BF16, sol.BF16 if grad is bf else sol.F32, 1 if accumulate else 0)
+    _call("sol_ffn_backward", dev, stream, desc)
 
 
 # ---------------------------------------------------------------------------------- AdamW

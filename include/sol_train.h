@@ -38,10 +38,23 @@ extern "C" {
 size_t sol_ffn_workspace_bytes(int64_t n_tokens, int64_t d, int64_t inner);
 
 /* Forward.  u may be NULL (serving: nothing kept for a backward pass). */
-sol_status sol_ffn(void* y, int64_t ld_y, void* u, int64_t ld_u, const void* x, int64_t ld_x,
-                   const void* w_up, int64_t ld_wu, const void* w_down, int64_t ld_wd,
-                   void* workspace, size_t workspace_bytes, int64_t n_tokens, int64_t d,
-                   int64_t inner, sol_dtype dt, sol_stream_t stream);
+typedef struct {
+    void* y;
+    int64_t ld_y; /* row strides in elements */
+    void* u;
+    int64_t ld_u;
+    const void* x;
+    int64_t ld_x;
+    const void* w_up;
+    int64_t ld_wu;
+    const void* w_down;
+    int64_t ld_wd;
+    void* workspace;
+    size_t workspace_bytes;
+    int64_t n_tokens, d, inner;
+    sol_dtype dt;
+} sol_ffn_desc;
+sol_status sol_ffn(const sol_ffn_desc* desc, sol_stream_t stream);
 
 /* Backward, from the u that the forward call kept (its bf16 values are the a and b of
  * these formulas):
@@ -53,12 +66,30 @@ sol_status sol_ffn(void* y, int64_t ld_y, void* u, int64_t ld_u, const void* x, 
  * (the sum is formed in fp32 and rounded once).  du and act are rounded to bf16 once, as
  * operands.  n_tokens == 0: the weight gradients are set to zero (accumulate: left as they
  * are), and dy, x, u and dx may be NULL. */
-sol_status sol_ffn_backward(void* dx, int64_t ld_dx, void* dw_up, int64_t ld_dwu, void* dw_down,
-                            int64_t ld_dwd, sol_dtype grad_dt, int32_t accumulate, const void* dy,
-                            int64_t ld_dy, const void* x, int64_t ld_x, const void* u, int64_t ld_u,
-                            const void* w_up, int64_t ld_wu, const void* w_down, int64_t ld_wd,
-                            void* workspace, size_t workspace_bytes, int64_t n_tokens, int64_t d,
-                            int64_t inner, sol_dtype dt, sol_stream_t stream);
+typedef struct {
+    void* dx;
+    int64_t ld_dx;
+    void* dw_up;
+    int64_t ld_dwu;
+    void* dw_down;
+    int64_t ld_dwd;
+    const void* dy;
+    int64_t ld_dy;
+    const void* x;
+    int64_t ld_x;
+    const void* u;
+    int64_t ld_u;
+    const void* w_up;
+    int64_t ld_wu;
+    const void* w_down;
+    int64_t ld_wd;
+    void* workspace;
+    size_t workspace_bytes;
+    int64_t n_tokens, d, inner;
+    sol_dtype dt, grad_dt;
+    int32_t accumulate;
+} sol_ffn_backward_desc;
+sol_status sol_ffn_backward(const sol_ffn_backward_desc* desc, sol_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * AdamW over many tensors at once (decoupled weight decay, Loshchilov and Hutter 2019).

@@ -53,7 +53,7 @@ FFN = dict(y=FAKE, ld_y=64, u=FAKE + STEP, ld_u=256, x=FAKE + 2 * STEP, ld_x=64,
 
 def ffn(L, **kw):
     a = {**FFN, **kw}
-    return L.sol_ffn(*a.values(), None)
+    return L.sol_ffn(ctypes.byref(train.FfnDesc(*a.values())), None)
 
 
 @pytest.mark.parametrize("kw,status,word", [
@@ -82,19 +82,30 @@ def test_ffn_refusals(L, kw, status, word):
     assert word in last(L), last(L)
 
 
+def test_descriptors_are_packed_as_they_are_declared(L):
+    """The bytes that the calls send against the structures' own, field by field."""
+    for of, pack in ((train.FfnDesc, train._pack_ffn), (train.FfnBackwardDesc, train._pack_ffn_backward)):
+        values = [i + 1 for i in range(len(of._fields_))]
+        assert pack(*values) == bytes(of(*values))
+    values = [.1, .2, .3, .4, 5, 6, 7, 8, 9]
+    assert train._pack_scalars(*values) == bytes(train.AdamwScalars(*values))
+    assert L.sol_ffn(None, None) == INV and "desc is NULL" in last(L)
+    assert L.sol_ffn_backward(None, None) == INV and "desc is NULL" in last(L)
+
+
 def test_ffn_of_no_tokens(L):
     assert ffn(L, n=0, x=None, y=None, u=None, ws=None, bytes=0) == sol.OK
 
 
-BWD = dict(dx=FAKE, ld_dx=64, dw_up=FAKE + STEP, ld_dwu=64, dw_down=FAKE + 2 * STEP, ld_dwd=128, gdt=sol.BF16, acc=0,
+BWD = dict(dx=FAKE, ld_dx=64, dw_up=FAKE + STEP, ld_dwu=64, dw_down=FAKE + 2 * STEP, ld_dwd=128,
            dy=FAKE + 3 * STEP, ld_dy=64, x=FAKE + 4 * STEP, ld_x=64, u=FAKE + 5 * STEP, ld_u=256, w_up=FAKE + 6 * STEP,
            ld_wu=64, w_down=FAKE + 7 * STEP, ld_wd=128, ws=FAKE + 8 * STEP, bytes=STEP, n=16, d=64, inner=128,
-           dt=sol.BF16)
+           dt=sol.BF16, gdt=sol.BF16, acc=0)
 
 
 def bwd(L, **kw):
     a = {**BWD, **kw}
-    return L.sol_ffn_backward(*a.values(), None)
+    return L.sol_ffn_backward(ctypes.byref(train.FfnBackwardDesc(*a.values())), None)
 
 
 @pytest.mark.parametrize("kw,status,word", [
