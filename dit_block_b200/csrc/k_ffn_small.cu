@@ -1,5 +1,5 @@
 // k_ffn_small.cu -- the gated feed-forward block for a few tokens (a denoising server's
-// smallest batches, single tokens): y = (silu(x Wg^T) * (x Wu^T)) Wd^T.
+// smallest batches, single tokens): y = (silu(x Wg^T) * (x Wu^T)) Wd^T, and its backward pass.
 //
 // Bound by the weights' bytes: 6 * d * inner of them against some tens of kilobytes of
 // everything else.  The weights are streamed once, straight from HBM to registers in rows of
@@ -9,11 +9,16 @@
 // matter as long as both operands agree, so that a lane's 16-byte vector of a weight row and
 // of a token's row are used as they come.
 //
-// A CTA takes 16 rows of weights (up projection: 8 of the gated half and the 8 of the other
+// A CTA takes up to 32 tokens and 16 rows of weights (up projection: 8 of the gated half and the 8 of the other
 // half that they meet, so that a thread ends up with a and b of the same value), its warps a
 // share of K each; the shares are added through shared memory in the order of the warps.
 // The second kernel is launched to overlap the first one's end (programmatic dependent
 // launch) and starts by loading weights, which do not depend on it.
+//
+// The backward pass for a few tokens in the same way: one kernel for d_act, du and act, one for dx and
+// the weight gradients, whose products over the tokens need no shared memory.  Bound by the launches and a
+// few loads that wait for each other (d 256, width 512, 32 tokens: 8.3 us, 16.2 as tiles of
+// k_ffn.cu), and by HBM at the block's full size (one token: 182 us for 850 MB, 4.7 TB/s).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -64,6 +69,8 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
     __shared__ float red[WARPS][16][8 * NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int32_t j0 = blockIdx.x * OUT;
+    const int32_t t0 = blockIdx.y * 8 * NT, T = min(p.T - t0, 8 * NT);  // this CTA's tokens
+    const bf16* px = p.x + t0 * p.ld_x;
     // rows g and g + 8 of the tensor instruction
     const int32_t ra = j0 + g, rb = UP ? p.rows + j0 + g : j0 + 8 + g;
     const bool la = ra < p.rows, lb = UP ? la : rb < p.rows;
@@ -94,8 +101,8 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
             const int32_t k = (c + i) * CHUNK + 8 * t;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const uint4 x = c + i < c1 && k < p.K && 8 * n + g < p.T
-                                    ? *reinterpret_cast<const uint4*>(p.x + (8 * n + g) * p.ld_x + k)
+                const uint4 x = c + i < c1 && k < p.K && 8 * n + g < T
+                                    ? *reinterpret_cast<const uint4*>(px + (8 * n + g) * p.ld_x + k)
                                     : zero;
                 mma(acc[n], a[i].x, b[i].x, a[i].y, b[i].y, x.x, x.y);
                 mma(acc[n], a[i].z, b[i].z, a[i].w, b[i].w, x.z, x.w);
@@ -111,8 +118,9 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
         red[warp][g + 8][8 * n + 2 * t + 1] = acc[n][3];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < OUT * p.T; i += 32 * WARPS) {
+    for (int i = threadIdx.x; i < OUT * T; i += 32 * WARPS) {
         const int j = i % OUT, n = i / OUT;
+        const int64_t row = t0 + n;
         if (j0 + j >= p.rows) continue;
         float v = 0.f, v2 = 0.f;
 #pragma unroll
@@ -122,12 +130,12 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
         }
         if (UP) {
             if (p.u) {
-                p.u[n * p.ld_u + j0 + j] = __float2bfloat16_rn(v);
-                p.u[n * p.ld_u + p.rows + j0 + j] = __float2bfloat16_rn(v2);
+                p.u[row * p.ld_u + j0 + j] = __float2bfloat16_rn(v);
+                p.u[row * p.ld_u + p.rows + j0 + j] = __float2bfloat16_rn(v2);
             }
             v = v / (1.f + __expf(-v)) * v2;
         }
-        p.out[n * p.ld_out + j0 + j] = __float2bfloat16_rn(v);
+        p.out[row * p.ld_out + j0 + j] = __float2bfloat16_rn(v);
     }
 }
 
@@ -138,7 +146,7 @@ template <bool UP, int WARPS> cudaError_t launch(const Params& p, bool after, cu
     la[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * WARPS);
-    cfg.gridDim = dim3((unsigned)((p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16)));
+    cfg.gridDim = dim3((unsigned)((p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16)), (unsigned)((p.T + 31) / 32));
     cfg.stream = s;
     cfg.attrs = la;
     cfg.numAttrs = after ? 1 : 0;
@@ -153,7 +161,268 @@ template <bool UP> cudaError_t launch(const Params& p, bool after, cudaStream_t 
     return (p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16) <= 148 ? launch<UP, 16>(p, after, s) : launch<UP, 8>(p, after, s);
 }
 
+// ---------------------------------------------------------------------------------
+// Backward.  Here the weights lie with the outputs' dimension contiguous and k from row to row: a
+// lane loads the same few columns of four rows, and byte permutations pair up two rows as the
+// tensor instruction wants them (a register holds two consecutive k).
+
+constexpr int BACK_WARPS = 8, BACK_N = 32;  // warps of a CTA; outputs a token of one (of d_act or dx)
+constexpr int GRAD_M = 64, GRAD_N = 32;     // a warp's tile of a weight gradient
+
+struct Back {
+    const bf16 *dy, *x, *u, *w_up, *w_down;
+    int64_t ld_dy, ld_x, ld_u, ld_wu, ld_wd;
+    bf16 *act, *du, *dx;
+    void *dw_up, *dw_down;
+    int64_t ld_dx, ld_dwu, ld_dwd;
+    int32_t T, d, inner;
+    int32_t out_f32, accumulate;
+    int32_t dx_ctas, up_tiles, down_tiles;  // work of k_back_grads
+};
+
+// Halfword `odd` of two words, the first in the lower half.
+__device__ __forceinline__ uint32_t pair_up(uint32_t lower, uint32_t upper, int odd)
+{
+    return __byte_perm(lower, upper, odd ? 0x7632 : 0x5410);
+}
+__device__ __forceinline__ uint32_t word(const uint2& v, int i) { return i ? v.y : v.x; }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i < 2 ? (i ? v.y : v.x) : (i == 2 ? v.z : v.w); }
+
+// The sum over warps, in red, of x[T, K] . w[K, N] for columns [n0, n0 + BACK_N): a warp's share of K, 16 at a
+// time.  Register e of a lane's column group stands for column 4 * group + e.  `dependent`: x is written by
+// the kernel before.
+template <int MT>
+__device__ __forceinline__ void rows_by_weights(float (&red)[BACK_WARPS][16 * MT][BACK_N + 1], const bf16* w, int64_t ld_w,
+                                                int32_t N, int32_t n0, const bf16* x, int64_t ld_x, int32_t T, int32_t K,
+                                                bool dependent)
+{
+    constexpr int U = 4;  // chunks in flight
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int32_t chunks = (K + 15) / 16, share = (chunks + BACK_WARPS - 1) / BACK_WARPS;
+    const int32_t c0 = min(warp * share, chunks), c1 = min(c0 + share, chunks);
+    const int32_t n = n0 + 4 * g;
+    const uint2 zero = make_uint2(0, 0);
+    float acc[MT][4][4] = {};
+    uint2 r[U][4];
+    auto weights = [&](int32_t c) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int32_t k = (c + i) * 16 + 4 * t;
+            const bool in = c + i < c1 && k < K && n < N;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                r[i][q] = in ? __ldg(reinterpret_cast<const uint2*>(w + (int64_t)(k + q) * ld_w + n)) : zero;
+        }
+    };
+    weights(c0);
+    if (dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int32_t c = c0; c < c1; c += U) {
+        if (c > c0) weights(c);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int32_t k = (c + i) * 16 + 4 * t;
+            const bool in = c + i < c1 && k < K;
+            uint2 a[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 16 * m + 8 * h + g;
+                    a[m][h] = in && row < T ? *reinterpret_cast<const uint2*>(x + row * ld_x + k) : zero;
+                }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b0 = pair_up(word(r[i][0], e / 2), word(r[i][1], e / 2), e & 1);
+                const uint32_t b1 = pair_up(word(r[i][2], e / 2), word(r[i][3], e / 2), e & 1);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma(acc[m][e], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, b0, b1);
+            }
+        }
+    }
+    // accumulator e: rows g, g + 8; the columns of groups 2t, 2t + 1
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[warp][16 * m + g + 8 * (v >> 1)][8 * t + 4 * (v & 1) + e] = acc[m][e][v];
+    __syncthreads();
+}
+
+// d_act = dy . W_down, and from it and u: du and act.
+template <int MT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_act(const __grid_constant__ Back p)
+{
+    __shared__ float red[BACK_WARPS][16 * MT][BACK_N + 1];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int OWN = 16 * MT * BACK_N / (32 * BACK_WARPS);  // values of a thread
+    const int32_t t0 = blockIdx.y * 16 * MT, T = min(p.T - t0, 16 * MT);  // this CTA's tokens
+    const int32_t n0 = blockIdx.x * BACK_N, n = n0 + (threadIdx.x & 31);
+    float a[OWN] = {}, b[OWN] = {};
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int row = (threadIdx.x >> 5) + i * BACK_WARPS;
+        if (row < T && n < p.inner) {
+            a[i] = __bfloat162float(p.u[(t0 + row) * p.ld_u + n]);
+            b[i] = __bfloat162float(p.u[(t0 + row) * p.ld_u + p.inner + n]);
+        }
+    }
+    rows_by_weights<MT>(red, p.w_down, p.ld_wd, p.inner, n0, p.dy + t0 * p.ld_dy, p.ld_dy, T, p.d, false);
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int row = (threadIdx.x >> 5) + i * BACK_WARPS;
+        if (row >= T || n >= p.inner) continue;
+        float d = 0.f;
+#pragma unroll
+        for (int w = 0; w < BACK_WARPS; ++w) d += red[w][row][threadIdx.x & 31];
+        const float s = 1.f / (1.f + __expf(-a[i])), as = a[i] * s;
+        const int64_t at = (int64_t)(t0 + row) * p.inner;
+        p.du[2 * at + n] = __float2bfloat16_rn(d * b[i] * s * fmaf(a[i], 1.f - s, 1.f));
+        p.du[2 * at + p.inner + n] = __float2bfloat16_rn(d * as);
+        p.act[at + n] = __float2bfloat16_rn(as * b[i]);
+    }
+}
+
+// Eight values of a weight gradient's row, from `at` on.
+__device__ __forceinline__ void put_grad(const Back& p, void* out, int64_t at, const float* v)
+{
+    float s[8];
+    if (p.out_f32) {
+        float* dst = static_cast<float*>(out) + at;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            unpack<float>(p.accumulate ? ld_plain(dst + 4 * h) : make_uint4(0, 0, 0, 0), s);
+            *reinterpret_cast<float4*>(dst + 4 * h) =
+                make_float4(s[0] + v[4 * h], s[1] + v[4 * h + 1], s[2] + v[4 * h + 2], s[3] + v[4 * h + 3]);
+        }
+    } else {
+        bf16* dst = static_cast<bf16*>(out) + at;
+        unpack<bf16>(p.accumulate ? ld_plain(dst) : make_uint4(0, 0, 0, 0), s);  // added in fp32, rounded once
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
+        *reinterpret_cast<uint4*>(dst) = pack<bf16>(s);
+    }
+}
+
+// One warp: a tile of GRAD_M x GRAD_N of a^T . b over the tokens; a [T, M], b [T, N].
+__device__ __forceinline__ void grad_tile(const Back& p, int32_t tile, const bf16* a, int64_t ld_a, int32_t M, const bf16* b,
+                                          int64_t ld_b, int32_t N, void* out, int64_t ld_out)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int32_t across = (N + GRAD_N - 1) / GRAD_N;
+    const int32_t m0 = tile / across * GRAD_M + 8 * g, n0 = tile % across * GRAD_N;
+    const bool in_m = m0 < M, in_n = n0 + 4 * g < N;
+    float acc[4][4][4] = {};
+    for (int32_t k0 = 0; k0 < p.T; k0 += 16) {
+        uint4 ra[4];
+        uint2 rb[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int32_t k = k0 + 4 * t + q;
+            ra[q] = k < p.T && in_m ? *reinterpret_cast<const uint4*>(a + k * ld_a + m0) : make_uint4(0, 0, 0, 0);
+            rb[q] = k < p.T && in_n ? *reinterpret_cast<const uint2*>(b + k * ld_b + n0 + 4 * g) : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {  // row groups: rows 8 * group + 2f, and 8 * group + 2f + 1 as the upper eight
+            const uint32_t a0 = pair_up(word(ra[0], f), word(ra[1], f), 0), a1 = pair_up(word(ra[0], f), word(ra[1], f), 1);
+            const uint32_t a2 = pair_up(word(ra[2], f), word(ra[3], f), 0), a3 = pair_up(word(ra[2], f), word(ra[3], f), 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mma(acc[f][e], a0, a1, a2, a3, pair_up(word(rb[0], e / 2), word(rb[1], e / 2), e & 1),
+                    pair_up(word(rb[2], e / 2), word(rb[3], e / 2), e & 1));
+        }
+    }
+    // a lane ends up with columns [8t, 8t + 8) of its eight rows
+    const int32_t n = n0 + 8 * t;
+    if (!in_m || n >= N) return;
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = acc[f][e & 3][2 * h + (e >> 2)];
+            put_grad(p, out, (m0 + 2 * f + h) * ld_out + n, v);
+        }
+}
+
+// dx = du . W_up by the first CTAs; a tile of dW_up = du^T . x or dW_down = dy^T . act by each warp of the others.
+template <int MT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_grads(const __grid_constant__ Back p)
+{
+    __shared__ float red[BACK_WARPS][16 * MT][BACK_N + 1];
+    if ((int)blockIdx.x < p.dx_ctas) {
+        const int32_t groups = (p.T + 16 * MT - 1) / (16 * MT), t0 = blockIdx.x % groups * 16 * MT, T = min(p.T - t0, 16 * MT);
+        const int32_t n0 = blockIdx.x / groups * BACK_N, n = n0 + (threadIdx.x & 31);
+        const int64_t ld_du = 2 * (int64_t)p.inner;
+        rows_by_weights<MT>(red, p.w_up, p.ld_wu, p.d, n0, p.du + t0 * ld_du, ld_du, T, 2 * p.inner, true);
+        for (int row = threadIdx.x >> 5; row < T; row += BACK_WARPS) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < BACK_WARPS; ++w) v += red[w][row][threadIdx.x & 31];
+            if (n < p.d) p.dx[(t0 + row) * p.ld_dx + n] = __float2bfloat16_rn(v);
+        }
+        return;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t tile = ((int)blockIdx.x - p.dx_ctas) * BACK_WARPS + (threadIdx.x >> 5);
+    if (tile < p.up_tiles)
+        grad_tile(p, tile, p.du, 2 * (int64_t)p.inner, 2 * p.inner, p.x, p.ld_x, p.d, p.dw_up, p.ld_dwu);
+    else if (tile < p.up_tiles + p.down_tiles)
+        grad_tile(p, tile - p.up_tiles, p.dy, p.ld_dy, p.d, p.act, p.inner, p.inner, p.dw_down, p.ld_dwd);
+}
+
+template <int MT> cudaError_t launch_back(const Back& p, cudaStream_t s)
+{
+    const unsigned groups = (unsigned)((p.T + 16 * MT - 1) / (16 * MT));
+    k_back_act<MT><<<dim3((p.inner + BACK_N - 1) / BACK_N, groups), 32 * BACK_WARPS, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(32 * BACK_WARPS);
+    cfg.gridDim = dim3((unsigned)(p.dx_ctas + (p.up_tiles + p.down_tiles + BACK_WARPS - 1) / BACK_WARPS));
+    cfg.stream = s;
+    cfg.attrs = la;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_back_grads<MT>, p);
+}
+
 }  // namespace ffn_small
+
+cudaError_t launch_ffn_small_backward(const FfnSmallBackward& f, cudaStream_t s)
+{
+    using namespace ffn_small;
+    const auto tiles = [](int32_t m, int32_t n) { return (m + GRAD_M - 1) / GRAD_M * ((n + GRAD_N - 1) / GRAD_N); };
+    Back p{};
+    p.dy = static_cast<const bf16*>(f.dy);
+    p.x = static_cast<const bf16*>(f.x);
+    p.u = static_cast<const bf16*>(f.u);
+    p.w_up = static_cast<const bf16*>(f.w_up);
+    p.w_down = static_cast<const bf16*>(f.w_down);
+    p.ld_dy = f.ld_dy;
+    p.ld_x = f.ld_x;
+    p.ld_u = f.ld_u;
+    p.ld_wu = f.ld_wu;
+    p.ld_wd = f.ld_wd;
+    p.act = static_cast<bf16*>(f.act);
+    p.du = static_cast<bf16*>(f.du);
+    p.dx = static_cast<bf16*>(f.dx);
+    p.dw_up = f.dw_up;
+    p.dw_down = f.dw_down;
+    p.ld_dx = f.ld_dx;
+    p.ld_dwu = f.ld_dwu;
+    p.ld_dwd = f.ld_dwd;
+    p.T = f.T;
+    p.d = f.d;
+    p.inner = f.inner;
+    p.out_f32 = f.out_f32;
+    p.accumulate = f.accumulate;
+    p.dx_ctas = f.dx ? (f.d + BACK_N - 1) / BACK_N * (f.T <= 16 ? 1 : (f.T + 31) / 32) : 0;
+    p.up_tiles = f.dw_up ? tiles(2 * f.inner, f.d) : 0;
+    p.down_tiles = f.dw_down ? tiles(f.d, f.inner) : 0;
+    return f.T <= 16 ? launch_back<1>(p, s) : launch_back<2>(p, s);
+}
 
 cudaError_t launch_ffn_small(const FfnSmall& f, cudaStream_t s)
 {

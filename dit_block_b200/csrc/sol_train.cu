@@ -240,6 +240,12 @@ sol_status sol_ffn_backward(const sol_ffn_backward_desc* desc, sol_stream_t stre
     if (!f.dx && !f.dw_up && !f.dw_down) return SOL_OK;
     void* act = (char*)f.workspace + lay.act;
     void* du = (char*)f.workspace + lay.du;
+    if (sol::ffn_small_backward_fits(T, d, inner)) {
+        const sol::FfnSmallBackward small{(int32_t)T, (int32_t)d, (int32_t)inner, f.dy, f.x, f.u, f.w_up, f.w_down,
+                                          f.ld_dy, f.ld_x, f.ld_u, f.ld_wu, f.ld_wd, act, du, f.dx, f.dw_up, f.dw_down,
+                                          f.ld_dx, f.ld_dwu, f.ld_dwd, f.grad_dt == SOL_DTYPE_F32, f.accumulate != 0};
+        return cuda_status(sol::launch_ffn_small_backward(small, s), "sol_ffn_backward launch");
+    }
     // d_act, and in its epilogue du and act
     sol::FfnProduct g = product(sol::FFN_DACT, T, inner, d, {f.dy, T, d, f.ld_dy}, false, {f.w_down, d, inner, f.ld_wd}, true,
                                 f.dw_down ? act : nullptr, inner, f.workspace, lay);

@@ -46,16 +46,22 @@ size_t ffn_slot_bytes(int64_t rows);
 // before on the stream is one of the same call, which may still be ending.
 cudaError_t launch_ffn_products(FfnProduct* g, int n, bool after, cudaStream_t s);
 
-// The whole forward pass for a few tokens (k_ffn_small.cu).  Measured at d x inner, us, against
-// k_ffn.cu:   1 token   5120 x 13824  69.8 : 83.5    1000 x 2504   6.0 : 19.0
-//            16 tokens  5120 x 13824  93 : 82.5      3000 x 8000  47 : 37     1000 x 2504   8.5 : 20
-//            32 tokens  5120 x 13824 142 : 85.6      1024 x 4096  15 : 20      256 x 512    5.7 : 9.2
-// k_ffn.cu takes some 14 us beside the weights' bytes at 6.2 TB/s; this one 3 us, with 6 TB/s for
-// up to 8 tokens, and about 3.3 and 2.2 TB/s for up to 16 and 32, where the tokens' values cost as
-// many loads as the weights: the two meet at 78 and 38 MB of weights.
+// The whole forward pass for a few tokens (k_ffn_small.cu).  Measured against k_ffn.cu, us, u kept:
+//     tokens      1           16          32          64          96          128         300
+//     64 x 64     3.1 : 8.2   3.8 : 8.3   4.8 : 8.3   4.9 : 8.5   4.9 : 8.8   4.9 : 9.1   5.0 : 8.7
+//     256 x 512   3.5 : 10.3  4.6 : 10.4  5.7 : 10.4  6.0 : 10.6  7.8 : 10.9  8.2 : 11.4  15.5 : 11.7
+//     568 x 936   3.9 : 14.1  5.3 : 14.2  7.0 : 14.2  9.4 : 15.0  11.8 : 16.4 14.1 : 17.9 29.7 : 18.2
+//     1000 x 2504 6.0 : 18.0  9.3 : 18.1  12.5 : 18.3 16.7 : 19.8 24.7 : 21.8 28.9 : 23.2
+//     3000 x 4000 17.9 : 28.6 26.1 : 28.8 31.8 : 29.6 57.5 : 31.1
+//     5120 x 13824 70 : 87    101 : 87    141 : 88
+// k_ffn.cu takes 8 to 14 us beside its k-blocks and the weights' bytes at 6.2 TB/s; this one 3 us, with 6 TB/s
+// for up to 8 tokens, and less the more of them, whose values cost as many loads as the weights.  Long rows of
+// W_down are few CTAs' work: 640 x 8800 takes 20.8 : 21.7 with 16 tokens, 26.3 : 21.9 with 32.
 inline bool ffn_small_fits(int64_t T, int64_t d, int64_t inner)
 {
-    return T <= 8 || (T <= 16 && d * inner <= 13000000) || (T <= 32 && d * inner <= 6300000);
+    if (T <= 8) return true;
+    const int64_t most = (T <= 64 ? 200000000 : T <= 128 ? 128000000 : 6000000) / T;
+    return T <= 512 && d * inner <= most && (T <= 16 || inner <= 8192);
 }
 struct FfnSmall {
     int32_t T, d, inner;
@@ -65,6 +71,31 @@ struct FfnSmall {
     int64_t ld_y, ld_u;
 };
 cudaError_t launch_ffn_small(const FfnSmall& f, cudaStream_t s);
+
+// The whole backward pass for a few tokens (k_ffn_small.cu), in two launches.  Measured as above, all gradients:
+//     tokens      1           16          32          64          96          128         200
+//     64 x 64     4.1 : 10.3  4.6 : 10.3  5.8 : 10.3  6.8 : 10.3  7.6 : 10.4  8.6 : 10.8  10.5 : 10.7
+//     256 x 512   5.2 : 16.2  6.1 : 16.3  8.3 : 16.2  8.3 : 16.4  9.1 : 16.8  10.2 : 17.3 13.3 : 16.9
+//     568 x 936   8.2 : 22.1  9.4 : 22.4  12.6 : 22.5 12.5 : 22.9 14.0 : 22.4 15.2 : 23.4 18.9 : 24.2
+//     1000 x 2504 16.1 : 38.4 17.4 : 38.7 23.7 : 38.9 26.9 : 39.4 30.9 : 33.7 35.9 : 35.2 53.2 : 37.5
+//     3000 x 4000 44 : 94     48 : 93     59 : 94     84 : 95     123 : 74
+//     5120 x 13824 182 : 288  213 : 288   293 : 291   464 : 292
+// and 640 x 8800, whose dx is 20 CTAs' work, 46.5 : 58.5 with 16 tokens, 65.0 : 57.8 with 32.
+inline bool ffn_small_backward_fits(int64_t T, int64_t d, int64_t inner)
+{
+    if (T <= 16) return d * inner < (int64_t)1 << 40;  // tiles of the gradients below 2^31
+    return T <= 224 && d * inner <= (T <= 64 ? 800000000 : 200000000) / T && inner <= 8192;
+}
+struct FfnSmallBackward {
+    int32_t T, d, inner;
+    const void *dy, *x, *u, *w_up, *w_down;
+    int64_t ld_dy, ld_x, ld_u, ld_wu, ld_wd;
+    void *act, *du;                // workspace [T, inner], [T, 2 * inner]
+    void *dx, *dw_up, *dw_down;    // each may be NULL
+    int64_t ld_dx, ld_dwu, ld_dwd;
+    bool out_f32, accumulate;      // of dw_up and dw_down
+};
+cudaError_t launch_ffn_small_backward(const FfnSmallBackward& f, cudaStream_t s);
 
 // Error flags raised by these kernels' bounded waits; optionally cleared.  Synchronous.
 uint32_t ffn_device_error(bool clear);

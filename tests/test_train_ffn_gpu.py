@@ -25,6 +25,10 @@ SIZES = [  # n_tokens, d, inner
     (63, 128, 64), (64, 128, 64), (65, 72, 64), (120, 64, 128), (128, 256, 512),
     (129, 64, 200), (257, 1000, 328), (1000, 200, 2504), (4099, 64, 64), (300, 2560, 1024), (20, 2000, 6008),
     (600, 1536, 4104),
+    # on both sides of where a few tokens end, in both directions
+    (32, 640, 8200), (33, 64, 72), (40, 3000, 8000), (57, 2048, 2048), (57, 3000, 5000), (63, 1000, 4000), (64, 2504, 5120),
+    (65, 1000, 3200), (96, 264, 520), (120, 1304, 1304), (128, 904, 1096), (200, 128, 256), (225, 64, 72),
+    (300, 64, 72), (513, 64, 72), (20, 5120, 8200),
 ]
 
 
@@ -310,7 +314,7 @@ def test_captured_and_replayed():
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("n,ld", [(16, (1 << 28) + (1 << 26)), (300, 1 << 24)])
+@pytest.mark.parametrize("n,ld", [(16, (1 << 28) + (1 << 26)), (300, 1 << 24), (600, 1 << 23)])
 def test_offsets_past_32_bits(n, ld):
     """Rows so far apart that elements lie more than 2^32 from the first: the bits of the same call on packed
     tensors."""
