@@ -12,17 +12,20 @@
 // A CTA takes up to 32 tokens and 16 rows of weights (up projection: 8 of the gated half and the 8 of the other
 // half that they meet, so that a thread ends up with a and b of the same value), its warps a
 // share of K each; the shares are added through shared memory in the order of the warps.
-// The second kernel is launched to overlap the first one's end (programmatic dependent
-// launch) and starts by loading weights, which do not depend on it.
+// Where that leaves most SMs without work (few outputs, long sums), a cluster of up to eight CTAs
+// shares the sums, which are added through distributed shared memory in the order of k (200 x 13000, one
+// token: 14.4 -> 8.7 us; its backward pass 45 -> 16).  The second kernel is launched to overlap the first one's
+// end (programmatic dependent launch) and starts by loading weights, which do not depend on it.
 //
 // The backward pass for a few tokens in the same way: one kernel for d_act, du and act, one for dx and
 // the weight gradients, whose products over the tokens need no shared memory.  Bound by the launches and a
-// few loads that wait for each other (d 256, width 512, 32 tokens: 8.3 us, 16.2 as tiles of
-// k_ffn.cu), and by HBM at the block's full size (one token: 182 us for 850 MB, 4.7 TB/s).
+// few loads that wait for each other (d 256, width 512, 32 tokens: 8.1 us, 15.8 as tiles of
+// k_ffn.cu), and by HBM at the block's full size (one token: 181 us for 850 MB, 4.7 TB/s).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 #include "train.h"
 
 namespace sol {
@@ -43,7 +46,25 @@ struct Params {
     bf16* u;  // up: kept u or NULL
     int64_t ld_u;
     int32_t T, rows, K;  // tokens; outputs a token (inner or d); inner dimension
+    int32_t split_log;   // 2^split_log CTAs (a cluster) share the K of the same outputs
 };
+
+// How many CTAs share the k of an output, as a power of two: more than one while they are at most `few`, and
+// while each still has `least` of it.
+int32_t split_of(int64_t ctas, int64_t few, int64_t k, int64_t least)
+{
+    int32_t log = 0;
+    while (log < 3 && ctas << log <= few && k >= (2 * least) << log) ++log;
+    return log;
+}
+
+// The same shared-memory word of CTA `rank` of the cluster.
+__device__ __forceinline__ float peer(const float& x, int rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::mapa(smem_u32(&x), rank)) : "memory");
+    return v;
+}
 
 __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -62,20 +83,21 @@ __device__ __forceinline__ uint4 ld_weights(const bf16* p)
     return v;
 }
 
-template <bool UP, int NT, int WARPS>
+template <bool UP, int NT, int WARPS, bool SPLIT>
 __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS) / WARPS) k_small(const __grid_constant__ Params p)
 {
     constexpr int OUT = UP ? 8 : 16;  // outputs a token of this CTA
     __shared__ float red[WARPS][16][8 * NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int32_t j0 = blockIdx.x * OUT;
+    const int32_t split = SPLIT ? 1 << p.split_log : 1, rank = (int)blockIdx.x & (split - 1);
+    const int32_t j0 = (SPLIT ? (int)blockIdx.x >> p.split_log : (int)blockIdx.x) * OUT;
     const int32_t t0 = blockIdx.y * 8 * NT, T = min(p.T - t0, 8 * NT);  // this CTA's tokens
     const bf16* px = p.x + t0 * p.ld_x;
     // rows g and g + 8 of the tensor instruction
     const int32_t ra = j0 + g, rb = UP ? p.rows + j0 + g : j0 + 8 + g;
     const bool la = ra < p.rows, lb = UP ? la : rb < p.rows;
-    const int32_t chunks = (p.K + CHUNK - 1) / CHUNK, share = (chunks + WARPS - 1) / WARPS;
-    const int32_t c0 = min(warp * share, chunks), c1 = min(c0 + share, chunks);
+    const int32_t chunks = (p.K + CHUNK - 1) / CHUNK, share = (chunks + split * WARPS - 1) / (split * WARPS);
+    const int32_t c0 = min((rank * WARPS + warp) * share, chunks), c1 = min(c0 + share, chunks);
     const bf16* wa = p.w + ra * p.ld_w + 8 * t;
     const bf16* wb = p.w + rb * p.ld_w + 8 * t;
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -118,15 +140,31 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
         red[warp][g + 8][8 * n + 2 * t + 1] = acc[n][3];
     }
     __syncthreads();
+    if constexpr (SPLIT) {  // this CTA's sum, over its first warp's, for the cluster to read
+        for (int i = threadIdx.x; i < 16 * T; i += 32 * WARPS) {
+            float v = 0.f;
+#pragma unroll
+            for (int s = 0; s < WARPS; ++s) v += red[s][i % 16][i / 16];
+            red[0][i % 16][i / 16] = v;
+        }
+        tc::cluster_sync();
+    }
     for (int i = threadIdx.x; i < OUT * T; i += 32 * WARPS) {
         const int j = i % OUT, n = i / OUT;
         const int64_t row = t0 + n;
-        if (j0 + j >= p.rows) continue;
+        if (j0 + j >= p.rows || (j & (split - 1)) != rank) continue;
         float v = 0.f, v2 = 0.f;
+        if constexpr (SPLIT) {  // in the order of k
+            for (int r = 0; r < split; ++r) {
+                v += peer(red[0][j][n], r);
+                if (UP) v2 += peer(red[0][j + 8][n], r);
+            }
+        } else {
 #pragma unroll
-        for (int s = 0; s < WARPS; ++s) {
-            v += red[s][j][n];
-            if (UP) v2 += red[s][j + 8][n];
+            for (int s = 0; s < WARPS; ++s) {
+                v += red[s][j][n];
+                if (UP) v2 += red[s][j + 8][n];
+            }
         }
         if (UP) {
             if (p.u) {
@@ -137,28 +175,35 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
         }
         p.out[row * p.ld_out + j0 + j] = __float2bfloat16_rn(v);
     }
+    if constexpr (SPLIT) tc::cluster_sync();  // the others may still be reading this CTA's sum
 }
 
-template <bool UP, int WARPS> cudaError_t launch(const Params& p, bool after, cudaStream_t s)
+template <bool UP, int NT, int WARPS> cudaError_t launch(Params p, bool after, cudaStream_t s)
 {
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    la[0].val.programmaticStreamSerializationAllowed = 1;
+    const int32_t across = (p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16), groups = (p.T + 8 * NT - 1) / (8 * NT);
+    p.split_log = split_of((int64_t)across * groups, 74, p.K, CHUNK * 2 * WARPS);
+    cudaLaunchAttribute la[3];
+    la[0].id = la[2].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = la[2].val.programmaticStreamSerializationAllowed = after;
+    la[1].id = cudaLaunchAttributeClusterDimension;
+    la[1].val.clusterDim.x = 1u << p.split_log;
+    la[1].val.clusterDim.y = la[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * WARPS);
-    cfg.gridDim = dim3((unsigned)((p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16)), (unsigned)((p.T + 31) / 32));
+    cfg.gridDim = dim3((unsigned)across << p.split_log, (unsigned)groups);
     cfg.stream = s;
-    cfg.attrs = la;
-    cfg.numAttrs = after ? 1 : 0;
-    return p.T <= 8    ? cudaLaunchKernelEx(&cfg, k_small<UP, 1, WARPS>, p)
-           : p.T <= 16 ? cudaLaunchKernelEx(&cfg, k_small<UP, 2, WARPS>, p)
-                       : cudaLaunchKernelEx(&cfg, k_small<UP, 4, WARPS>, p);
+    cfg.attrs = p.split_log ? la + 1 : la;
+    cfg.numAttrs = (after ? 1 : 0) + (p.split_log ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, p.split_log ? k_small<UP, NT, WARPS, true> : k_small<UP, NT, WARPS, false>, p);
 }
 
 // Sixteen warps a CTA where there is at most one CTA an SM, else eight.
 template <bool UP> cudaError_t launch(const Params& p, bool after, cudaStream_t s)
 {
-    return (p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16) <= 148 ? launch<UP, 16>(p, after, s) : launch<UP, 8>(p, after, s);
+    const bool few = (p.rows + (UP ? 7 : 15)) / (UP ? 8 : 16) <= 148;
+    if (p.T <= 8) return few ? launch<UP, 1, 16>(p, after, s) : launch<UP, 1, 8>(p, after, s);
+    if (p.T <= 16) return few ? launch<UP, 2, 16>(p, after, s) : launch<UP, 2, 8>(p, after, s);
+    return few ? launch<UP, 4, 16>(p, after, s) : launch<UP, 4, 8>(p, after, s);
 }
 
 // ---------------------------------------------------------------------------------
@@ -167,6 +212,7 @@ template <bool UP> cudaError_t launch(const Params& p, bool after, cudaStream_t 
 // tensor instruction wants them (a register holds two consecutive k).
 
 constexpr int BACK_WARPS = 8, BACK_N = 32;  // warps of a CTA; outputs a token of one (of d_act or dx)
+constexpr int BACK_FEW = 80;                // CTAs of a product up to which two share the k of an output
 constexpr int GRAD_M = 64, GRAD_N = 32;     // a warp's tile of a weight gradient
 
 struct Back {
@@ -178,7 +224,9 @@ struct Back {
     int32_t T, d, inner;
     int32_t out_f32, accumulate;
     int32_t dx_ctas, up_tiles, down_tiles;  // work of k_back_grads
+    int32_t split_log;                      // 2^split_log CTAs (a cluster) share the k of the same outputs
 };
+template <int MT> using Red = float[BACK_WARPS][16 * MT][BACK_N + 1];
 
 // Halfword `odd` of two words, the first in the lower half.
 __device__ __forceinline__ uint32_t pair_up(uint32_t lower, uint32_t upper, int odd)
@@ -188,18 +236,18 @@ __device__ __forceinline__ uint32_t pair_up(uint32_t lower, uint32_t upper, int 
 __device__ __forceinline__ uint32_t word(const uint2& v, int i) { return i ? v.y : v.x; }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i < 2 ? (i ? v.y : v.x) : (i == 2 ? v.z : v.w); }
 
-// The sum over warps, in red, of x[T, K] . w[K, N] for columns [n0, n0 + BACK_N): a warp's share of K, 16 at a
-// time.  Register e of a lane's column group stands for column 4 * group + e.  `dependent`: x is written by
+// x[T, K] . w[K, N] for columns [n0, n0 + BACK_N), a warp's share of K at a time: each warp's sum in red.  `rank`
+// of the `split` CTAs of a cluster.  Register e of a lane's column group stands for column 4 * group + e.  `dependent`: x is written by
 // the kernel before.
-template <int MT>
-__device__ __forceinline__ void rows_by_weights(float (&red)[BACK_WARPS][16 * MT][BACK_N + 1], const bf16* w, int64_t ld_w,
-                                                int32_t N, int32_t n0, const bf16* x, int64_t ld_x, int32_t T, int32_t K,
+template <int MT, bool SPLIT>
+__device__ __forceinline__ void rows_by_weights(Red<MT>& red, const bf16* w, int64_t ld_w, int32_t N, int32_t n0,
+                                                const bf16* x, int64_t ld_x, int32_t T, int32_t K, int32_t rank, int32_t split,
                                                 bool dependent)
 {
     constexpr int U = 4;  // chunks in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int32_t chunks = (K + 15) / 16, share = (chunks + BACK_WARPS - 1) / BACK_WARPS;
-    const int32_t c0 = min(warp * share, chunks), c1 = min(c0 + share, chunks);
+    const int32_t chunks = (K + 15) / 16, share = (chunks + split * BACK_WARPS - 1) / (split * BACK_WARPS);
+    const int32_t c0 = min((rank * BACK_WARPS + warp) * share, chunks), c1 = min(c0 + share, chunks);
     const int32_t n = n0 + 4 * g;
     const uint2 zero = make_uint2(0, 0);
     float acc[MT][4][4] = {};
@@ -247,39 +295,60 @@ __device__ __forceinline__ void rows_by_weights(float (&red)[BACK_WARPS][16 * MT
 #pragma unroll
             for (int v = 0; v < 4; ++v) red[warp][16 * m + g + 8 * (v >> 1)][8 * t + 4 * (v & 1) + e] = acc[m][e][v];
     __syncthreads();
+    if (!SPLIT) return;
+    // this CTA's sum, over its first warp's, for the cluster to read
+    for (int row = warp; row < T; row += BACK_WARPS) {
+        float v = 0.f;
+#pragma unroll
+        for (int s = 0; s < BACK_WARPS; ++s) v += red[s][row][lane];
+        red[0][row][lane] = v;
+    }
+    tc::cluster_sync();
+}
+// An output's value, the sums in the order of k.
+template <int MT, bool SPLIT> __device__ __forceinline__ float summed(Red<MT>& red, int row, int col, int split)
+{
+    float v = 0.f;
+    if (!SPLIT) {
+#pragma unroll
+        for (int s = 0; s < BACK_WARPS; ++s) v += red[s][row][col];
+    } else {
+        for (int r = 0; r < split; ++r) v += peer(red[0][row][col], r);
+    }
+    return v;
 }
 
 // d_act = dy . W_down, and from it and u: du and act.
-template <int MT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_act(const __grid_constant__ Back p)
+template <int MT, bool SPLIT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_act(const __grid_constant__ Back p)
 {
-    __shared__ float red[BACK_WARPS][16 * MT][BACK_N + 1];
+    const int32_t split = SPLIT ? 1 << p.split_log : 1, rank = (int)blockIdx.x & (split - 1);
+    __shared__ Red<MT> red;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int OWN = 16 * MT * BACK_N / (32 * BACK_WARPS);  // values of a thread
     const int32_t t0 = blockIdx.y * 16 * MT, T = min(p.T - t0, 16 * MT);  // this CTA's tokens
-    const int32_t n0 = blockIdx.x * BACK_N, n = n0 + (threadIdx.x & 31);
+    const int32_t n0 = (SPLIT ? (int)blockIdx.x >> p.split_log : (int)blockIdx.x) * BACK_N, n = n0 + (threadIdx.x & 31);
     float a[OWN] = {}, b[OWN] = {};
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
         const int row = (threadIdx.x >> 5) + i * BACK_WARPS;
-        if (row < T && n < p.inner) {
+        if (row < T && n < p.inner && (row & (split - 1)) == rank) {
             a[i] = __bfloat162float(p.u[(t0 + row) * p.ld_u + n]);
             b[i] = __bfloat162float(p.u[(t0 + row) * p.ld_u + p.inner + n]);
         }
     }
-    rows_by_weights<MT>(red, p.w_down, p.ld_wd, p.inner, n0, p.dy + t0 * p.ld_dy, p.ld_dy, T, p.d, false);
+    rows_by_weights<MT, SPLIT>(red, p.w_down, p.ld_wd, p.inner, n0, p.dy + t0 * p.ld_dy, p.ld_dy, T, p.d, rank, split, false);
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
         const int row = (threadIdx.x >> 5) + i * BACK_WARPS;
-        if (row >= T || n >= p.inner) continue;
-        float d = 0.f;
-#pragma unroll
-        for (int w = 0; w < BACK_WARPS; ++w) d += red[w][row][threadIdx.x & 31];
+        if (row >= T || n >= p.inner || (row & (split - 1)) != rank) continue;
+        const float d = summed<MT, SPLIT>(red, row, threadIdx.x & 31, split);
         const float s = 1.f / (1.f + __expf(-a[i])), as = a[i] * s;
         const int64_t at = (int64_t)(t0 + row) * p.inner;
         p.du[2 * at + n] = __float2bfloat16_rn(d * b[i] * s * fmaf(a[i], 1.f - s, 1.f));
         p.du[2 * at + p.inner + n] = __float2bfloat16_rn(d * as);
         p.act[at + n] = __float2bfloat16_rn(as * b[i]);
     }
+    if (SPLIT) tc::cluster_sync();  // the others may still be reading this CTA's sum
 }
 
 // Eight values of a weight gradient's row, from `at` on.
@@ -346,20 +415,22 @@ __device__ __forceinline__ void grad_tile(const Back& p, int32_t tile, const bf1
 }
 
 // dx = du . W_up by the first CTAs; a tile of dW_up = du^T . x or dW_down = dy^T . act by each warp of the others.
-template <int MT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_grads(const __grid_constant__ Back p)
+template <int MT, bool SPLIT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_grads(const __grid_constant__ Back p)
 {
-    __shared__ float red[BACK_WARPS][16 * MT][BACK_N + 1];
+    __shared__ Red<MT> red;
     if ((int)blockIdx.x < p.dx_ctas) {
-        const int32_t groups = (p.T + 16 * MT - 1) / (16 * MT), t0 = blockIdx.x % groups * 16 * MT, T = min(p.T - t0, 16 * MT);
-        const int32_t n0 = blockIdx.x / groups * BACK_N, n = n0 + (threadIdx.x & 31);
+        const int32_t split = SPLIT ? 1 << p.split_log : 1, rank = (int)blockIdx.x & (split - 1);
+        const int32_t at = SPLIT ? (int)blockIdx.x >> p.split_log : (int)blockIdx.x;
+        const int32_t groups = (p.T + 16 * MT - 1) / (16 * MT), t0 = at % groups * 16 * MT, T = min(p.T - t0, 16 * MT);
+        const int32_t n0 = at / groups * BACK_N, n = n0 + (threadIdx.x & 31);
         const int64_t ld_du = 2 * (int64_t)p.inner;
-        rows_by_weights<MT>(red, p.w_up, p.ld_wu, p.d, n0, p.du + t0 * ld_du, ld_du, T, 2 * p.inner, true);
+        rows_by_weights<MT, SPLIT>(red, p.w_up, p.ld_wu, p.d, n0, p.du + t0 * ld_du, ld_du, T, 2 * p.inner, rank, split, true);
         for (int row = threadIdx.x >> 5; row < T; row += BACK_WARPS) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < BACK_WARPS; ++w) v += red[w][row][threadIdx.x & 31];
+            if ((row & (split - 1)) != rank) continue;
+            const float v = summed<MT, SPLIT>(red, row, threadIdx.x & 31, split);
             if (n < p.d) p.dx[(t0 + row) * p.ld_dx + n] = __float2bfloat16_rn(v);
         }
+        if (SPLIT) tc::cluster_sync();
         return;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -370,22 +441,34 @@ template <int MT> __global__ void __launch_bounds__(32 * BACK_WARPS) k_back_grad
         grad_tile(p, tile - p.up_tiles, p.dy, p.ld_dy, p.d, p.act, p.inner, p.inner, p.dw_down, p.ld_dwd);
 }
 
-template <int MT> cudaError_t launch_back(const Back& p, cudaStream_t s)
+template <int MT> cudaError_t launch_back(Back p, cudaStream_t s)
 {
-    const unsigned groups = (unsigned)((p.T + 16 * MT - 1) / (16 * MT));
-    k_back_act<MT><<<dim3((p.inner + BACK_N - 1) / BACK_N, groups), 32 * BACK_WARPS, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute la[1];
+    const int32_t groups = (p.T + 16 * MT - 1) / (16 * MT);
+    cudaLaunchAttribute la[2];
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     la[0].val.programmaticStreamSerializationAllowed = 1;
+    la[1].id = cudaLaunchAttributeClusterDimension;
+    la[1].val.clusterDim.y = la[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * BACK_WARPS);
-    cfg.gridDim = dim3((unsigned)(p.dx_ctas + (p.up_tiles + p.down_tiles + BACK_WARPS - 1) / BACK_WARPS));
     cfg.stream = s;
+    int32_t across = (p.inner + BACK_N - 1) / BACK_N;
+    p.split_log = split_of((int64_t)across * groups, BACK_FEW, p.d, 16 * 4 * BACK_WARPS);
+    la[1].val.clusterDim.x = 1u << p.split_log;
+    cfg.gridDim = dim3((unsigned)across << p.split_log, (unsigned)groups);
+    cfg.attrs = la + 1;
+    cfg.numAttrs = p.split_log ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, p.split_log ? k_back_act<MT, true> : k_back_act<MT, false>, p);
+    if (e != cudaSuccess) return e;
+    across = p.dx ? (p.d + BACK_N - 1) / BACK_N : 0;
+    p.split_log = across ? split_of((int64_t)across * groups, BACK_FEW, 2 * (int64_t)p.inner, 16 * 4 * BACK_WARPS) : 0;
+    p.dx_ctas = across * groups << p.split_log;
+    const int32_t grads = (p.up_tiles + p.down_tiles + BACK_WARPS - 1) / BACK_WARPS;
+    la[1].val.clusterDim.x = 1u << p.split_log;
+    cfg.gridDim = dim3((unsigned)(p.dx_ctas + (grads + (1 << p.split_log) - 1 >> p.split_log << p.split_log)));
     cfg.attrs = la;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_back_grads<MT>, p);
+    cfg.numAttrs = p.split_log ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, p.split_log ? k_back_grads<MT, true> : k_back_grads<MT, false>, p);
 }
 
 }  // namespace ffn_small
@@ -418,7 +501,6 @@ cudaError_t launch_ffn_small_backward(const FfnSmallBackward& f, cudaStream_t s)
     p.inner = f.inner;
     p.out_f32 = f.out_f32;
     p.accumulate = f.accumulate;
-    p.dx_ctas = f.dx ? (f.d + BACK_N - 1) / BACK_N * (f.T <= 16 ? 1 : (f.T + 31) / 32) : 0;
     p.up_tiles = f.dw_up ? tiles(2 * f.inner, f.d) : 0;
     p.down_tiles = f.dw_down ? tiles(f.d, f.inner) : 0;
     return f.T <= 16 ? launch_back<1>(p, s) : launch_back<2>(p, s);

@@ -48,20 +48,20 @@ cudaError_t launch_ffn_products(FfnProduct* g, int n, bool after, cudaStream_t s
 
 // The whole forward pass for a few tokens (k_ffn_small.cu).  Measured against k_ffn.cu, us, u kept:
 //     tokens      1           16          32          64          96          128         300
-//     64 x 64     3.1 : 8.2   3.8 : 8.3   4.8 : 8.3   4.9 : 8.5   4.9 : 8.8   4.9 : 9.1   5.0 : 8.7
-//     256 x 512   3.5 : 10.3  4.6 : 10.4  5.7 : 10.4  6.0 : 10.6  7.8 : 10.9  8.2 : 11.4  15.5 : 11.7
-//     568 x 936   3.9 : 14.1  5.3 : 14.2  7.0 : 14.2  9.4 : 15.0  11.8 : 16.4 14.1 : 17.9 29.7 : 18.2
-//     1000 x 2504 6.0 : 18.0  9.3 : 18.1  12.5 : 18.3 16.7 : 19.8 24.7 : 21.8 28.9 : 23.2
-//     3000 x 4000 17.9 : 28.6 26.1 : 28.8 31.8 : 29.6 57.5 : 31.1
+//     64 x 64     3.2 : 8.2   3.8 : 8.3   4.7 : 8.4   4.8 : 8.6   5.0 : 8.8   4.9 : 9.1   5.0 : 8.7
+//     256 x 512   3.4 : 10.4  4.6 : 10.5  5.7 : 10.5  6.1 : 10.7  7.8 : 11.0  8.1 : 11.3  15.5 : 11.7
+//     568 x 936   3.9 : 14.0  5.4 : 14.1  7.0 : 14.1  9.6 : 15.0  11.7 : 16.3 14.1 : 17.8 29.7 : 18.2
+//     1000 x 2504 6.4 : 18.0  9.4 : 18.2  12.9 : 18.3 16.6 : 20.0 24.7 : 21.8 28.9 : 23.2
+//     3000 x 4000 18.1 : 28.7 26.3 : 29.0 31.8 : 29.6 57.5 : 31.1
 //     5120 x 13824 70 : 87    101 : 87    141 : 88
 // k_ffn.cu takes 8 to 14 us beside its k-blocks and the weights' bytes at 6.2 TB/s; this one 3 us, with 6 TB/s
 // for up to 8 tokens, and less the more of them, whose values cost as many loads as the weights.  Long rows of
-// W_down are few CTAs' work: 640 x 8800 takes 20.8 : 21.7 with 16 tokens, 26.3 : 21.9 with 32.
+// W_down are few CTAs' work: 200 x 13000 takes 20.0 : 20.9 with 32 tokens, 33.5 : 23.6 with 64.
 inline bool ffn_small_fits(int64_t T, int64_t d, int64_t inner)
 {
     if (T <= 8) return true;
     const int64_t most = (T <= 64 ? 200000000 : T <= 128 ? 128000000 : 6000000) / T;
-    return T <= 512 && d * inner <= most && (T <= 16 || inner <= 8192);
+    return T <= 512 && d * inner <= most && (T <= 32 || inner <= 8192);
 }
 struct FfnSmall {
     int32_t T, d, inner;
@@ -74,17 +74,17 @@ cudaError_t launch_ffn_small(const FfnSmall& f, cudaStream_t s);
 
 // The whole backward pass for a few tokens (k_ffn_small.cu), in two launches.  Measured as above, all gradients:
 //     tokens      1           16          32          64          96          128         200
-//     64 x 64     4.1 : 10.3  4.6 : 10.3  5.8 : 10.3  6.8 : 10.3  7.6 : 10.4  8.6 : 10.8  10.5 : 10.7
-//     256 x 512   5.2 : 16.2  6.1 : 16.3  8.3 : 16.2  8.3 : 16.4  9.1 : 16.8  10.2 : 17.3 13.3 : 16.9
-//     568 x 936   8.2 : 22.1  9.4 : 22.4  12.6 : 22.5 12.5 : 22.9 14.0 : 22.4 15.2 : 23.4 18.9 : 24.2
-//     1000 x 2504 16.1 : 38.4 17.4 : 38.7 23.7 : 38.9 26.9 : 39.4 30.9 : 33.7 35.9 : 35.2 53.2 : 37.5
-//     3000 x 4000 44 : 94     48 : 93     59 : 94     84 : 95     123 : 74
-//     5120 x 13824 182 : 288  213 : 288   293 : 291   464 : 292
-// and 640 x 8800, whose dx is 20 CTAs' work, 46.5 : 58.5 with 16 tokens, 65.0 : 57.8 with 32.
+//     64 x 64     4.0 : 10.5  4.5 : 10.3  5.7 : 10.3  6.7 : 10.4  7.5 : 10.5  8.8 : 10.8  10.5 : 10.7
+//     256 x 512   5.1 : 15.9  6.1 : 15.8  8.1 : 15.8  8.5 : 16.0  10.0 : 16.4 11.5 : 17.0 13.3 : 16.9
+//     568 x 936   7.5 : 22.4  8.6 : 22.6  11.0 : 22.8 12.4 : 23.3 13.6 : 22.7 15.7 : 23.9 18.9 : 24.2
+//     1000 x 2504 13.3 : 38.5 14.8 : 38.6 19.1 : 38.7 25.3 : 39.2 30.9 : 33.7 35.9 : 35.2 53.2 : 37.5
+//     640 x 8800  20.8 : 56.8 25.0 : 57.0 33.3 : 57.2 50.9 : 57.9 91.5 : 46.8
+//     3000 x 4000 44 : 94     48 : 93     59 : 94     84 : 96     123 : 74
+//     5120 x 13824 181 : 288  214 : 290   293 : 291   464 : 292
 inline bool ffn_small_backward_fits(int64_t T, int64_t d, int64_t inner)
 {
     if (T <= 16) return d * inner < (int64_t)1 << 40;  // tiles of the gradients below 2^31
-    return T <= 224 && d * inner <= (T <= 64 ? 800000000 : 200000000) / T && inner <= 8192;
+    return T <= 224 && d * inner <= (T <= 64 ? 800000000 : 200000000) / T;
 }
 struct FfnSmallBackward {
     int32_t T, d, inner;

@@ -28,7 +28,7 @@ SIZES = [  # n_tokens, d, inner
     # on both sides of where a few tokens end, in both directions
     (32, 640, 8200), (33, 64, 72), (40, 3000, 8000), (57, 2048, 2048), (57, 3000, 5000), (63, 1000, 4000), (64, 2504, 5120),
     (65, 1000, 3200), (96, 264, 520), (120, 1304, 1304), (128, 904, 1096), (200, 128, 256), (225, 64, 72),
-    (300, 64, 72), (513, 64, 72), (20, 5120, 8200),
+    (300, 64, 72), (513, 64, 72), (20, 5120, 8200), (1, 64, 13000), (13, 200, 13000), (30, 3448, 200), (5, 5120, 64), (40, 184, 12000),
 ]
 
 
