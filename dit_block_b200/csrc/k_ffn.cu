@@ -17,8 +17,8 @@
 // time is least.
 //
 // At d 5120, width 13,824 and 31,248 tokens: forward with u kept 10.2 ms (1.30 PFLOP/s), backward
-// 21.5 ms (1.23), both at the power cap, where cuBLAS alone reaches 1.38; at 1,252 tokens 0.47 and
-// 0.95 ms; 32 tokens of d 256, width 512: 5.8 us on the GPU.
+// 21.5 ms (1.23), both at the power cap, where cuBLAS alone reaches 1.38; at 1,252 tokens 0.48 and
+// 0.97 ms; few tokens of small blocks go to k_ffn_small.cu.
 // Everything outside a tensor is read as zero by the tensor copies (ragged M, N and K) and
 // never stored.
 //
