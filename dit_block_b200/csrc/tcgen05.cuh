@@ -88,10 +88,12 @@ __device__ __forceinline__ void commit(uint32_t bar)
 // Warp-collective load of 32 consecutive 32-bit columns of this warp's 32 TMEM lanes:
 // lane i of the warp gets row (taddr.lane + i), columns taddr.col .. +31.  The wait for
 // the load sits in the same asm statement, so no use of the registers can be scheduled
-// before the data arrived.
+// before the data arrived.  The lanes meet first: an epilogue's loop may have sent some of
+// them past the stores of a row behind the last one, or one lane into a tensor copy.
 __device__ __forceinline__ void ld32(uint32_t taddr, float* v)
 {
     uint32_t r[32];
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
