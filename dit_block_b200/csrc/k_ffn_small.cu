@@ -58,13 +58,6 @@ int32_t split_of(int64_t ctas, int64_t few, int64_t k, int64_t least)
     return log;
 }
 
-// Every thread of the cluster; the warps may come out of a loop of unequal lanes.
-__device__ __forceinline__ void cluster_meet()
-{
-    __syncwarp();
-    tc::cluster_sync();
-}
-
 // The same shared-memory word of CTA `rank` of the cluster.
 __device__ __forceinline__ float peer(const float& x, int rank)
 {
@@ -154,7 +147,7 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
             for (int s = 0; s < WARPS; ++s) v += red[s][i % 16][i / 16];
             red[0][i % 16][i / 16] = v;
         }
-        cluster_meet();
+        tc::cluster_sync();
     }
     for (int i = threadIdx.x; i < OUT * T; i += 32 * WARPS) {
         const int j = i % OUT, n = i / OUT;
@@ -182,7 +175,7 @@ __global__ void __launch_bounds__(32 * WARPS, (NT > 2 ? SM_WARPS / 2 : SM_WARPS)
         }
         p.out[row * p.ld_out + j0 + j] = __float2bfloat16_rn(v);
     }
-    if constexpr (SPLIT) cluster_meet();  // the others may still be reading this CTA's sum
+    if constexpr (SPLIT) tc::cluster_sync();  // the others may still be reading this CTA's sum
 }
 
 template <bool UP, int NT, int WARPS> cudaError_t launch(Params p, bool after, cudaStream_t s)
@@ -310,7 +303,7 @@ __device__ __forceinline__ void rows_by_weights(Red<MT>& red, const bf16* w, int
         for (int s = 0; s < BACK_WARPS; ++s) v += red[s][row][lane];
         red[0][row][lane] = v;
     }
-    cluster_meet();
+    tc::cluster_sync();
 }
 // An output's value, the sums in the order of k.
 template <int MT, bool SPLIT> __device__ __forceinline__ float summed(Red<MT>& red, int row, int col, int split)
@@ -355,7 +348,7 @@ template <int MT, bool SPLIT> __global__ void __launch_bounds__(32 * BACK_WARPS)
         p.du[2 * at + p.inner + n] = __float2bfloat16_rn(d * as);
         p.act[at + n] = __float2bfloat16_rn(as * b[i]);
     }
-    if (SPLIT) cluster_meet();  // the others may still be reading this CTA's sum
+    if (SPLIT) tc::cluster_sync();  // the others may still be reading this CTA's sum
 }
 
 // Eight values of a weight gradient's row, from `at` on.
@@ -437,7 +430,7 @@ template <int MT, bool SPLIT> __global__ void __launch_bounds__(32 * BACK_WARPS)
             const float v = summed<MT, SPLIT>(red, row, threadIdx.x & 31, split);
             if (n < p.d) p.dx[(t0 + row) * p.ld_dx + n] = __float2bfloat16_rn(v);
         }
-        if (SPLIT) cluster_meet();
+        if (SPLIT) tc::cluster_sync();
         return;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");

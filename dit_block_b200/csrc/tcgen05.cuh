@@ -36,22 +36,26 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t m, uint32_t n)
 }
 
 // ---------------------------------------------------------------------------------
-// Tensor memory.  Allocation and release are warp-collective (.sync.aligned).
+// Tensor memory.  Allocation and release are warp-collective (.sync.aligned); the lanes meet
+// first, since one of them may have issued the MMAs alone.
 
 // Allocate `ncols` columns (a power of two, 32..512); the TMEM address is written to
 // the shared-memory word at `dst_smem`.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols)
 {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                  "r"(ncols)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_relinquish()
 {
+    __syncwarp();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
 {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                  : "memory");
 }
@@ -184,9 +188,11 @@ __device__ __forceinline__ uint32_t mapa(uint32_t smem_addr, uint32_t rank)
     return r;
 }
 
-// Every thread of both CTAs (release / acquire at cluster scope).
+// Every thread of the cluster (release / acquire at cluster scope).  A warp's lanes meet first:
+// they may come out of a loop that they left one by one, or that one of them ran alone.
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -194,15 +200,18 @@ __device__ __forceinline__ void cluster_sync()
 // same shared-memory destination; both CTAs get the same columns.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols)
 {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_relinquish_pair()
 {
+    __syncwarp();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
 {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 

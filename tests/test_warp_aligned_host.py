@@ -20,7 +20,9 @@ def functions_with(text: str, instruction: str):
         yield text[start:at]
 
 
-@pytest.mark.parametrize("instruction", ["tcgen05.ld.sync.aligned"])
+@pytest.mark.parametrize("instruction", [
+    "tcgen05.ld.sync.aligned", "tcgen05.alloc.", "tcgen05.relinquish_alloc_permit.", "tcgen05.dealloc.",
+    "barrier.cluster.arrive.release.aligned"])
 def test_lanes_meet_before_a_warp_aligned_instruction(instruction):
     found = 0
     for path in sorted(glob.glob(os.path.join(build.CSRC, "*.cu")) + glob.glob(os.path.join(build.CSRC, "*.cuh"))):
