@@ -336,16 +336,18 @@ __device__ __forceinline__ float block_scale(float top)
 }
 
 // How a block's values are brought to units of the table's first step (`most` of them make up the
-// scale s): x * inv; for a small s, where most / s would overflow, x * 2^100 first.  A scale of
-// zero or NaN gives zero codes.
+// scale s): x * inv; for a small s, where most / s would overflow, x * 2^100 first.  What is inverted is s * down:
+// the reciprocal of an s above 2^126 would be flushed.  A scale of zero or NaN gives zero codes.
 struct Unit {
-    float pre, inv;
+    float down, inv;
+    __device__ __forceinline__ bool small() const { return down > 1.f; }
 };
+constexpr float SMALL = 0x1p100f, DOWN = 0x1p-24f;
 __device__ __forceinline__ Unit unit_of(float s, float most)
 {
     Unit u;
-    u.pre = s < 1e-28f ? 1.2676506e30f : 1.f;
-    u.inv = s > 0.f ? most * rcp_ftz(s * u.pre) : 0.f;  // off by 2^-22: the margin of 2^-20 covers it
+    u.down = s < 1e-28f ? SMALL * DOWN : DOWN;
+    u.inv = s > 0.f ? (most * DOWN) * rcp_ftz(s * u.down) : 0.f;  // off by 2^-22: the margin of 2^-20 covers it
     return u;
 }
 // The codes of a lane's eight new moments (two runs of four, HALF apart; `at`: the hash's argument for the
@@ -361,8 +363,8 @@ __device__ __forceinline__ void encode8(float2* m, float2* v, uint32_t at, uint2
     n1 = block_scale(top1);
     n2 = block_scale(top2);
     const Unit u1 = unit_of(n1, 16129.f), u2 = unit_of(n2, 4228250625.f);
-    if (u1.pre != 1.f) scale8(m, u1.pre);
-    if (u2.pre != 1.f) scale8(v, u2.pre);
+    if (u1.small()) scale8(m, SMALL);
+    if (u2.small()) scale8(v, SMALL);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         float2 z[4], up[4];
