@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <limits>
 #include <new>
 #include <utility>
 #include <vector>
@@ -392,6 +393,9 @@ sol_status sol_adamw_step(const sol_adamw_plan* plan, const sol_adamw_scalars* h
     CHECK(h, SOL_ERR_INVALID_ARGUMENT, "scalars is NULL");
     CHECK(std::isfinite(h->lr) && std::isfinite(h->eps) && h->eps >= 0, SOL_ERR_INVALID_ARGUMENT,
           "lr must be finite, eps finite and >= 0");
+    // a divisor below fp32's normal numbers is taken for zero, which makes 0 / (0 + eps) NaN
+    CHECK(h->eps == 0 || h->eps >= std::numeric_limits<float>::min(), SOL_ERR_INVALID_ARGUMENT,
+          "eps (%g) must be 0 or at least 2^-126", h->eps);
     CHECK(h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1, SOL_ERR_INVALID_ARGUMENT,
           "beta1 and beta2 must be in [0, 1)");
     CHECK(h->step >= 1, SOL_ERR_INVALID_ARGUMENT, "step (%lld) must be at least 1", (long long)h->step);

@@ -97,9 +97,11 @@ sol_status sol_ffn_backward(const sol_ffn_backward_desc* desc, sol_stream_t stre
  *     m = beta1 * m + (1 - beta1) * g
  *     v = beta2 * v + (1 - beta2) * g^2
  *     p = p - lr * (weight_decay * p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
- * in fp32.  Parameters are f32; a tensor may have a bf16 copy of them that the step writes
- * too (what the linear layers read).  A parameter kept in bf16 alone is not supported: an
- * update below half a step of its format would be lost.
+ * in fp32: v / (1 - beta2^step) above fp32's range (gradients of some 1e19 at the first steps) gives no
+ * update, and with eps 0 a value that had no gradient so far moves by 0 / 0.  Parameters are f32; a
+ * tensor may have a bf16 copy of them that the step writes too (what the linear layers read).  A
+ * parameter kept in bf16 alone is not supported: an update below half a step of its format would be
+ * lost.
  *
  * Moments: f32, or 8 bits a value (state_bits 8).  In 8 bits a tensor is cut into blocks
  * of SOL_ADAMW_BLOCK values, each with one f32 scale s, the block's largest magnitude:
@@ -132,7 +134,7 @@ typedef struct {
  * grad_factor (device, or NULL for 1) multiplies every gradient, such as the second value
  * of sol_adamw_grad_norm. */
 typedef struct {
-    double lr, beta1, beta2, eps; /* finite; 0 <= beta < 1; eps >= 0 */
+    double lr, beta1, beta2, eps; /* finite; 0 <= beta < 1; eps 0 or >= 2^-126, fp32's least normal number */
     int64_t step;                /* >= 1: the number of this step */
     uint64_t seed;               /* of the 8-bit rounding */
     const float* lr_device;

@@ -58,3 +58,22 @@ def test_first_moments_with_a_scale_near_the_end_of_fp32(n, top):
     assert neighbours(m.abs(), s, tables()[0], got.abs(), 32 * U * s).all()
     assert ((got.abs().amax(1, keepdim=True) - s).abs() <= 8 * U * s).all(), "the largest of a block"
     assert blocks_of(torch.ones(n, device="cuda"), n)[v.isnan()].sum() == n
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30, 1e-13])
+def test_small_eps(bits, eps):
+    """Values that never had a gradient stay as they are, the others move as the formula says, whatever eps."""
+    n = 600
+    t = tensors([n], bits=bits)
+    for k in ("m", "v"):
+        t[k][0].zero_()
+    t["grads"][0][::3] = 0
+    p, g = t["params"][0].clone(), t["grads"][0].clone()
+    zero = torch.zeros(n, device="cuda")
+    want, _, _ = formula(p, g, zero, zero, 0.0, 1, eps=eps)
+    with train.AdamW(**t) as opt:
+        opt.step(step=1, lr=1e-3, eps=eps)
+    got = t["params"][0]
+    assert torch.equal(got[::3], p[::3])
+    assert ((got.to(F64) - want[0]).abs() <= want[1])[g != 0].all()

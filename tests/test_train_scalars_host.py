@@ -1,0 +1,26 @@
+"""Host-side checks of an AdamW step's scalars (no GPU: each call is refused, at last for want of a plan)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+from dit_block_b200 import build, sol
+from test_train_host import last, scalars
+
+from dit_block_b200 import train
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return train.lib()
+
+
+@pytest.mark.parametrize("eps,word", [
+    (5e-324, "eps"), (1e-50, "eps"), (1e-45, "eps"), (1e-39, "eps"), (1.17e-38, "eps"),  # zero or subnormal in fp32
+    (0.0, "plan is NULL"), (2.0 ** -126, "plan is NULL"), (1e-30, "plan is NULL"), (1e-8, "plan is NULL"),
+])
+def test_eps_is_zero_or_a_normal_number_of_fp32(L, eps, word):
+    assert L.sol_adamw_step(None, ctypes.byref(scalars(eps=eps)), None) == sol.ERR_INVALID_ARGUMENT
+    assert word in last(L), last(L)
