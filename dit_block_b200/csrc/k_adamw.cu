@@ -611,9 +611,11 @@ __global__ void __launch_bounds__(THREADS) k_norm_final(float* out, const double
     for (int i = threadIdx.x; i < n; i += THREADS) sum += partial[i];
     sum = cta_sum(sum, buf);
     if (threadIdx.x == 0) {
-        const double norm = sqrt(sum), f = (double)max_norm / (norm + 1e-6);
+        const double norm = sqrt(sum);
+        // without a limit nothing is clipped, not by infinity / infinity either; a NaN stays
+        const double f = isinf(max_norm) && isinf(norm) ? 1.0 : (double)max_norm / (norm + 1e-6);
         out[0] = (float)norm;
-        out[1] = f > 1.0 ? 1.f : (float)f;  // a NaN stays
+        out[1] = f > 1.0 ? 1.f : (float)f;
     }
 }
 

@@ -158,7 +158,8 @@ sol_status sol_adamw_step(const sol_adamw_plan* plan, const sol_adamw_scalars* s
 
 /* Global norm of the plan's gradients and the factor that clips it:
  *     out[0] = sqrt(sum of g^2 over all tensors),  out[1] = min(1, max_norm / (out[0] + 1e-6))
- * (device f32 [2], 8-byte aligned; a NaN norm gives a NaN factor).  Squares are scaled, so
+ * (device f32 [2], 8-byte aligned; a NaN norm gives a NaN factor, and with an infinite max_norm any
+ * other norm, an infinite one too, gives 1).  Squares are scaled, so
  * that no gradient of f32's range overflows or vanishes; sums are formed in fp64, in a fixed
  * order.  workspace: SOL_ADAMW_NORM_WORKSPACE bytes, 16-byte aligned, apart from out; calls that may
  * overlap need one each.  max_norm > 0, finite or infinite. */

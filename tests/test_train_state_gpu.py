@@ -1,0 +1,45 @@
+"""GPU tests of what calls leave behind: the fine-tuning object after captures and refused calls, and the clip factor
+where nothing is clipped."""
+from __future__ import annotations
+
+import gc
+import weakref
+
+import pytest
+import torch
+
+from dit_block_b200 import finetune, sol, train
+from test_finetune_gpu import BF, tokens, weights
+from test_train_adamw_gpu import norm_of, tensors
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def test_nothing_is_clipped_without_a_limit():
+    """max_norm infinite: the factor is 1 for an infinite norm too, so that the gradient that made it so stays
+    with its own value; a NaN norm still shows."""
+    one = lambda *v: [torch.tensor(v, device="cuda")]  # noqa: E731
+    assert norm_of(one(INF, 1.0), max_norm=INF) == [INF, 1.0]
+    assert norm_of(one(-INF, 0.0), max_norm=INF) == [INF, 1.0]
+    assert norm_of(one(torch.finfo(torch.float32).max, 0.0), max_norm=INF)[1] == 1.0
+    n, f = norm_of(one(float("nan"), 1.0), max_norm=INF)
+    assert n != n and f != f
+    assert norm_of(one(INF, 1.0), max_norm=1e38) == [INF, 0.0]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_infinite_gradient_stays_with_its_value(bits):
+    t = tensors([1000, 300], bits=bits)
+    t["grads"][0][700] = INF
+    with train.AdamW(**t) as opt:
+        out = torch.zeros(2, device="cuda")
+        opt.grad_norm(out, INF, workspace=opt.norm_workspace())
+        opt.step(step=1, lr=1e-3, grad_factor=out[1:])
+    bad = t["params"][0].isnan()
+    assert bad[700] and bad.sum() == 1 and torch.isfinite(t["params"][1]).all()
+
+
+def parts(ff, dy):
+    return [t.clone() for t in (ff.backward(dy), *ff.grads)]
