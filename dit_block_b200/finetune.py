@@ -84,13 +84,18 @@ class FeedForward:
 
     def capture(self, x: torch.Tensor, dy: torch.Tensor, max_norm: float = float("inf")) -> torch.cuda.CUDAGraph:
         """A CUDA graph of forward, backward and update over the buffers x and dy, whose contents and ``self.lr``
-        may change between replays.  Nothing runs now.  The graph uses this object's buffers: replays must not
-        overlap its other calls, and it must not outlive ``close``."""
+        may change between replays.  Nothing runs now, and the last forward stays the one that ``backward`` belongs to.
+        The graph uses this object's buffers: replays must not overlap its other calls, and it must not outlive
+        ``close``."""
         g = torch.cuda.CUDAGraph()
-        with torch.cuda.device(self.lr.device), torch.cuda.graph(g):
-            self.forward(x)
-            self.backward(dy)
-            self.update(max_norm)
+        last = self._x
+        try:
+            with torch.cuda.device(self.lr.device), torch.cuda.graph(g):
+                self.forward(x)
+                self.backward(dy)
+                self.update(max_norm)
+        finally:
+            self._x = last
         return g
 
     def moments(self, dtype: torch.dtype = torch.float32):

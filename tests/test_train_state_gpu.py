@@ -43,3 +43,25 @@ def test_an_infinite_gradient_stays_with_its_value(bits):
 
 def parts(ff, dy):
     return [t.clone() for t in (ff.backward(dy), *ff.grads)]
+
+
+def test_a_capture_leaves_the_last_forward_as_it_was():
+    ff = finetune.FeedForward(*weights(), 64)
+    x, dy = tokens(64, 1), tokens(64, 2, std=0.1)
+    ff.forward(x)
+    want = parts(ff, dy)
+    ff.forward(x)
+    other = ff.capture(tokens(40, 3), tokens(40, 4))
+    for a, b in zip(parts(ff, dy), want):
+        assert torch.equal(a, b)
+    del other
+    ff.close()
+
+
+def test_a_capture_is_no_forward():
+    ff = finetune.FeedForward(*weights(), 8)
+    graph = ff.capture(tokens(8, 1), tokens(8, 2))
+    with pytest.raises(RuntimeError, match="forward before"):
+        ff.backward(tokens(8, 2))
+    del graph
+    ff.close()
