@@ -63,8 +63,9 @@ class FeedForward:
         n = x.shape[0]
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens are more than max_tokens ({self.max_tokens})")
-        self._x = x
-        return train.ffn(self.y[:n], x, *self.weights, u=self.u[:n], workspace=self.workspace)
+        y = train.ffn(self.y[:n], x, *self.weights, u=self.u[:n], workspace=self.workspace)
+        self._x = x  # a call that was refused has not touched u
+        return y
 
     def backward(self, dy: torch.Tensor, accumulate: bool = False) -> torch.Tensor:
         """dx (in this object's buffer) of the last forward's tokens; the weight gradients are set, or with accumulate added to."""

@@ -65,3 +65,18 @@ def test_a_capture_is_no_forward():
         ff.backward(tokens(8, 2))
     del graph
     ff.close()
+
+
+def test_a_refused_forward_leaves_the_last_one_as_it_was():
+    ff = finetune.FeedForward(*weights(), 64)
+    x, dy = tokens(64, 1), tokens(64, 2, std=0.1)
+    y = ff.forward(x)
+    want = parts(ff, dy)
+    ff.forward(x)
+    with pytest.raises(sol.SolError, match="overlaps"):
+        ff.forward(y)
+    with pytest.raises(TypeError, match="x must be"):
+        ff.forward(x.float())
+    for a, b in zip(parts(ff, dy), want):
+        assert torch.equal(a, b)
+    ff.close()
