@@ -78,10 +78,14 @@ class FeedForward:
 
     def update(self, max_norm: float = float("inf")) -> None:
         """One AdamW step at the learning rate ``self.lr`` holds, gradients clipped to a norm of max_norm."""
-        self.step.add_(1)
         self.optimizer.grad_norm(self.norm, max_norm, workspace=self.norm_workspace)
-        self.optimizer.step(lr=0.0, betas=self.betas, eps=self.eps, step=1, seed=self.seed, lr_device=self.lr,
-                            step_device=self.step, grad_factor=self.norm[1:])
+        self.step.add_(1)
+        try:
+            self.optimizer.step(lr=0.0, betas=self.betas, eps=self.eps, step=1, seed=self.seed, lr_device=self.lr,
+                                step_device=self.step, grad_factor=self.norm[1:])
+        except Exception:
+            self.step.sub_(1)  # a refused step does not count
+            raise
 
     def capture(self, x: torch.Tensor, dy: torch.Tensor, max_norm: float = float("inf")) -> torch.cuda.CUDAGraph:
         """A CUDA graph of forward, backward and update over the buffers x and dy, whose contents and ``self.lr``

@@ -80,3 +80,25 @@ def test_a_refused_forward_leaves_the_last_one_as_it_was():
     for a, b in zip(parts(ff, dy), want):
         assert torch.equal(a, b)
     ff.close()
+
+
+def test_a_refused_update_is_no_step():
+    a, b = (finetune.FeedForward(*weights(), 8) for _ in range(2))
+    x, dy = tokens(8, 1), tokens(8, 2)
+    for ff in (a, b):
+        ff.lr.fill_(1e-3)
+        ff.forward(x)
+        ff.backward(dy)
+    with pytest.raises(sol.SolError, match="max_norm"):
+        a.update(-1.0)
+    a.betas = (0.9, 1.0)
+    with pytest.raises(sol.SolError, match="beta1 and beta2"):
+        a.update(1.0)
+    a.betas = b.betas
+    assert int(a.step) == 0
+    for ff in (a, b):
+        ff.update(1.0)
+    for p, q in zip(a.params, b.params):
+        assert torch.equal(p, q)
+    a.close()
+    b.close()
