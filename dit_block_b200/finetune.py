@@ -18,6 +18,12 @@ from . import train
 BF16 = torch.bfloat16
 
 
+class StepGraph(torch.cuda.CUDAGraph):
+    """A captured training step, and what its replays read."""
+
+    reads: tuple
+
+
 class FeedForward:
     """A gated feed-forward block in training: w_up [2 * inner, d] (gated half first), w_down [d, inner]."""
 
@@ -91,8 +97,9 @@ class FeedForward:
         """A CUDA graph of forward, backward and update over the buffers x and dy, whose contents and ``self.lr``
         may change between replays.  Nothing runs now, and the last forward stays the one that ``backward`` belongs to.
         The graph uses this object's buffers: replays must not overlap its other calls, and it must not outlive
-        ``close``."""
-        g = torch.cuda.CUDAGraph()
+        ``close``.  It keeps this object, x and dy alive."""
+        g = StepGraph()
+        g.reads = (self, x, dy)
         last = self._x
         try:
             with torch.cuda.device(self.lr.device), torch.cuda.graph(g):

@@ -102,3 +102,19 @@ def test_a_refused_update_is_no_step():
         assert torch.equal(p, q)
     a.close()
     b.close()
+
+
+def test_a_graph_keeps_what_it_reads():
+    """The buffers that a captured step reads live as long as the graph, whoever else holds them."""
+    ff = finetune.FeedForward(*weights(), 8)
+    x, dy = tokens(8, 1), tokens(8, 2)
+    seen = [weakref.ref(t) for t in (x, dy, ff)]
+    graph = ff.capture(x, dy)
+    del x, dy, ff
+    gc.collect()
+    assert all(r() is not None for r in seen)
+    graph.replay()
+    torch.cuda.synchronize()
+    del graph
+    gc.collect()
+    assert all(r() is None for r in seen)
