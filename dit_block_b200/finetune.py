@@ -23,6 +23,10 @@ class StepGraph(torch.cuda.CUDAGraph):
 
     reads: tuple
 
+    def replay(self) -> None:
+        super().replay()
+        self.reads[0]._x = None  # its u is no longer that of an eager forward
+
 
 class FeedForward:
     """A gated feed-forward block in training: w_up [2 * inner, d] (gated half first), w_down [d, inner]."""
@@ -95,7 +99,8 @@ class FeedForward:
 
     def capture(self, x: torch.Tensor, dy: torch.Tensor, max_norm: float = float("inf")) -> torch.cuda.CUDAGraph:
         """A CUDA graph of forward, backward and update over the buffers x and dy, whose contents and ``self.lr``
-        may change between replays.  Nothing runs now, and the last forward stays the one that ``backward`` belongs to.
+        may change between replays.  Nothing runs now, and the last forward stays the one that ``backward`` belongs to;
+        after a replay ``backward`` needs a forward of its own.
         The graph uses this object's buffers: replays must not overlap its other calls, and it must not outlive
         ``close``.  It keeps this object, x and dy alive."""
         g = StepGraph()

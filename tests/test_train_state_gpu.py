@@ -118,3 +118,19 @@ def test_a_graph_keeps_what_it_reads():
     del graph
     gc.collect()
     assert all(r() is None for r in seen)
+
+
+def test_a_replay_ends_the_last_forward():
+    """A replay writes the pre-activation that an eager backward would read, and new weights."""
+    ff = finetune.FeedForward(*weights(), 8)
+    x, dy = tokens(8, 1), tokens(8, 2)
+    graph = ff.capture(x, dy)
+    ff.forward(tokens(8, 3))
+    graph.replay()
+    with pytest.raises(RuntimeError, match="forward before"):
+        ff.backward(dy)
+    ff.forward(x)
+    ff.backward(dy)
+    torch.cuda.synchronize()
+    del graph
+    ff.close()
