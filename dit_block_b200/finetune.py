@@ -49,7 +49,7 @@ class FeedForward:
         self.m = [torch.zeros(p.shape, dtype=first, device=dev) for p in self.params]
         self.v = [torch.zeros(p.shape, dtype=second, device=dev) for p in self.params]
         scales = lambda: None if state_bits == 32 else [  # noqa: E731
-            torch.zeros(-(-p.numel() // train.BLOCK), device=dev) for p in self.params]
+            torch.zeros(-(-p.numel() // train.BLOCK), dtype=torch.float32, device=dev) for p in self.params]
         self.m_scales, self.v_scales = scales(), scales()
         self.optimizer = train.AdamW(self.params, self.grads, self.m, self.v, m_scales=self.m_scales,
                                      v_scales=self.v_scales, copies=self.weights, weight_decay=weight_decay)
@@ -57,8 +57,8 @@ class FeedForward:
         self.norm_workspace = self.optimizer.norm_workspace()
         empty = lambda cols: torch.empty((max_tokens, cols), dtype=BF16, device=dev)  # noqa: E731
         self.y, self.u, self.dx = empty(d), empty(2 * inner), empty(d)
-        self.norm = torch.zeros(2, device=dev)       # of the last update's gradients, and its clip factor
-        self.lr = torch.zeros(1, device=dev)
+        self.norm = torch.zeros(2, dtype=torch.float32, device=dev)  # of the last update's gradients, and its clip factor
+        self.lr = torch.zeros(1, dtype=torch.float32, device=dev)
         self.step = torch.zeros(1, dtype=torch.int64, device=dev)
         self._x = None
 

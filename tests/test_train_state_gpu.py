@@ -120,6 +120,22 @@ def test_a_graph_keeps_what_it_reads():
     assert all(r() is None for r in seen)
 
 
+@pytest.mark.parametrize("default", [BF, torch.float64])
+def test_buffers_do_not_follow_the_default_type(default):
+    w = weights()
+    torch.set_default_dtype(default)
+    try:
+        ff = finetune.FeedForward(*w, 8, state_bits=8)
+        ff.lr.fill_(1e-3)
+        ff.forward(tokens(8, 1))
+        ff.backward(tokens(8, 2).to(BF))
+        ff.update(1.0)
+        assert int(ff.step) == 1 and ff.moments()[0][0].dtype is torch.float32
+    finally:
+        torch.set_default_dtype(torch.float32)
+    ff.close()
+
+
 def test_a_replay_ends_the_last_forward():
     """A replay writes the pre-activation that an eager backward would read, and new weights."""
     ff = finetune.FeedForward(*weights(), 8)
