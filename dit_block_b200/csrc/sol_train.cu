@@ -373,7 +373,17 @@ try {
 sol_status sol_adamw_plan_destroy(sol_adamw_plan* plan)
 {
     if (!plan) return SOL_OK;
-    const cudaError_t e = plan->dev ? cudaFree(plan->dev) : cudaSuccess;
+    cudaError_t e = cudaSuccess;
+    if (plan->dev) {
+        // a plan may be let go of while some stream is captured, which has nothing to do with it: without this the
+        // capture would be spoilt
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        e = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e == cudaSuccess) {
+            e = cudaFree(plan->dev);
+            cudaThreadExchangeStreamCaptureMode(&mode);
+        }
+    }
     delete plan;
     return cuda_status(e, "sol_adamw_plan_destroy");
 }

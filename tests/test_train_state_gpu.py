@@ -150,3 +150,24 @@ def test_a_replay_ends_the_last_forward():
     torch.cuda.synchronize()
     del graph
     ff.close()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_plan_let_go_of_during_a_capture(bits):
+    """Freeing a plan that the captured stream does not use, as the garbage collector may at any time."""
+    t, ref = tensors([1000], bits=bits), tensors([1000], bits=bits)
+    opt, other = train.AdamW(**t), train.AdamW(**tensors([500], bits=bits))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step(step=1, lr=1e-3)
+        other.close()
+        opt.step(step=2, lr=1e-3)
+    graph.replay()
+    with train.AdamW(**ref) as eager:
+        for step in (1, 2):
+            eager.step(step=step, lr=1e-3)
+    torch.cuda.synchronize()
+    for k in t:
+        assert torch.equal(t[k][0], ref[k][0]), k
+    del graph
+    opt.close()
