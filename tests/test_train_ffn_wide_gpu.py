@@ -74,3 +74,29 @@ def test_backward(n, d, inner, grad_type, accumulate, pad):
         assert torch.equal(alone, again)
         for k in bf:  # and a bf16 gradient is the f32 one, rounded once
             assert torch.equal(bf[k], f32[k].to(BF)), k
+
+
+def test_pre_activations_past_32_bits():
+    """80,000 tokens of width 13,824: u and du hold more than 2^31 values.  dy is zero but for the first and the last
+    tokens, so that the weight gradients are those tokens' alone; zero terms of a sum add no error."""
+    n, d, inner, ends = 80_000, 64, 13_824, 150
+    assert 2 * n * inner > 1 << 31
+    i = inputs(n, d, inner)
+    some = torch.cat([torch.arange(ends), torch.arange(n - ends, n)]).cuda()
+    y, u = run_forward(i)
+    u64, eu, y64, ey = forward64(i["x"][some], i["w_up"], i["w_down"])
+    close(u[some], u64, eu, "u")
+    close(y[some], y64, ey, "y")
+    dy = torch.zeros((n, d), device="cuda", dtype=BF)
+    dy[some] = drawn(4, 2 * ends, d, 0.1)
+    out = grads(n, d, inner, F32)
+    train.ffn_backward(dy, i["x"], u, i["w_up"], i["w_down"], workspace=train.ffn_workspace(n, d, inner), **out)
+    want = backward64(dy[some], i["x"][some], u[some], i["w_up"], i["w_down"])
+    assert (out["dx"][ends:-ends] == 0).all()
+    out["dx"] = out["dx"][some]
+    for k, got in out.items():
+        g, e = want[k]
+        rounding = HALF if got.dtype == BF else 2.0 ** -24
+        close(got, g, 1.01 * (e + rounding * (g.abs() + e)) + 1e-30, k)
+    del u, y, out, want
+    torch.cuda.empty_cache()

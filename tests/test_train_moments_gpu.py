@@ -60,6 +60,79 @@ def test_first_moments_with_a_scale_near_the_end_of_fp32(n, top):
     assert blocks_of(torch.ones(n, device="cuda"), n)[v.isnan()].sum() == n
 
 
+@pytest.mark.parametrize("grad_type", [torch.float32, BF])
+def test_only_small_second_moments_are_stored_as_one(grad_type):
+    """A value above the table's first step is stored as one of its two neighbours, no lower; one below it as
+    that step, not as zero."""
+    sizes = [3, 255, 257, 1000, 4097]
+    t = tensors(sizes, grad_type, seed=2, bits=8)
+    with train.AdamW(**t) as opt:
+        opt.step(step=1, seed=11, **HYPER)
+        for k, n in enumerate(sizes):
+            g = t["grads"][k].to(F64)
+            v = blocks_of(g * g * 1e-3, n)
+            _, got, _, s = stored(t, k)
+            second = tables()[1]
+            low = second[1] * s
+            small = v <= low * (1 + 2.0 ** -20)
+            assert small.any() or n < 10
+            near = neighbours(v, s, second, got, 32 * U * s * (v / s).clamp(min=float(second[1])))
+            assert (near | small).all()
+            assert (((got - low).abs() <= 32 * U * low) | ~small | (v == 0)).all()
+
+
+@pytest.mark.parametrize("n", [100, 300, 511])
+def test_rounding_of_a_last_block_is_unbiased(n):
+    """As for whole blocks: the mean over R draws is off by at most 5 h / (2 sqrt(R)) and 2^-16 h, h the table's step."""
+    draws = 400
+    g = torch.randn(n, device="cuda", generator=gen(n))
+    sums = torch.zeros(2, n, device="cuda", dtype=F64)
+    for seed in range(draws):
+        t = tensors([n], bits=8)
+        t["grads"][0].copy_(g)
+        with train.AdamW(**t) as opt:
+            opt.step(step=1, seed=seed, **HYPER)
+            sums += torch.stack(decode(t, 0)).to(F64)
+    mean = sums / draws
+    for value, table, got, floor in ((g.to(F64) * 0.1, tables()[0], mean[0], 0.0), (g.to(F64) ** 2 * 0.001, tables()[1], mean[1], 1.0)):
+        x = blocks_of(value.abs(), n)
+        s = x.amax(1, keepdim=True)
+        k = (torch.searchsorted(table, x / s, right=True) - 1).clamp(0, len(table) - 2)
+        h = (table[k + 1] - table[k]) * s
+        bound = 5 * h / (2 * draws ** 0.5) + h * 2.0 ** -16 + 64 * U * s + floor * table[1] * s
+        assert ((blocks_of(got.abs(), n) - x).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("sizes", [[1000, 5000], [70, 2_000_000]])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_counted_on_the_device_are_the_host_counted_ones(sizes, bits):
+    """Few chunks count the step in each CTA, many in a kernel ahead: parameters, moments or their codes and
+    scales, and copies, bit for bit those of calls with the host's step."""
+    t, ref = tensors(sizes, BF, bits=bits), tensors(sizes, BF, bits=bits)
+    copies, ref_copies = ([torch.zeros(n, device="cuda", dtype=BF) for n in sizes] for _ in range(2))
+    lr, step, factor = torch.tensor([1e-3], device="cuda"), torch.tensor([1], device="cuda"), torch.tensor([0.5], device="cuda")
+    opt = train.AdamW(**t, copies=copies, weight_decay=0.01)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step(lr=0.5, step=77, seed=3, lr_device=lr, step_device=step, grad_factor=factor)
+        step.add_(1)
+    with train.AdamW(**ref, copies=ref_copies, weight_decay=0.01) as other:
+        for n in range(1, 6):
+            for x, y in zip(t["grads"], ref["grads"]):
+                x.copy_(torch.randn(x.numel(), device="cuda", generator=gen(n)))
+                y.copy_(x)
+            graph.replay()
+            other.step(lr=float(lr), step=n, seed=3, grad_factor=factor)
+    torch.cuda.synchronize()
+    for k in t:
+        for a, b in zip(t[k], ref[k]):
+            assert torch.equal(a, b), k
+    assert all(torch.equal(a, b) for a, b in zip(copies, ref_copies))
+    assert all((p != q).any() for p, q in zip(t["params"], tensors(sizes, BF, bits=bits)["params"]))
+    del graph
+    opt.close()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30, 1e-13])
 def test_small_eps(bits, eps):
