@@ -152,7 +152,7 @@ def ffn_workspace(n_tokens: int, d: int, inner: int, device=None) -> torch.Tenso
     nb = ffn_workspace_bytes(n_tokens, d, inner)
     if nb == 0:
         raise ValueError("d and inner must be multiples of 8, n_tokens >= 0")
-    return torch.empty((nb,), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty((nb,), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def ffn(y, x, w_up, w_down, *, u=None, workspace, stream=None):

@@ -24,3 +24,12 @@ def L():
 def test_eps_is_zero_or_a_normal_number_of_fp32(L, eps, word):
     assert L.sol_adamw_step(None, ctypes.byref(scalars(eps=eps)), None) == sol.ERR_INVALID_ARGUMENT
     assert word in last(L), last(L)
+
+
+@pytest.mark.parametrize("device,want", [(None, "cuda"), (0, 0), ("cuda:0", "cuda:0"), (1, 1)])
+def test_a_workspace_lies_on_the_device_asked_for(L, monkeypatch, device, want):
+    """Device 0 is a device, not "the current one"."""
+    asked = []
+    monkeypatch.setattr(train.torch, "empty", lambda *a, device, **kw: asked.append(device))
+    train.ffn_workspace(4, 64, 64, device=device)
+    assert asked == [want] and type(asked[0]) is type(want)
