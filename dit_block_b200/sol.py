@@ -465,7 +465,7 @@ def adaln_workspace(n_tokens: int, n_out: int, d: int, *, n_streams=1, tokens_pe
     nb = adaln_workspace_bytes(n_tokens, n_out, d, n_streams=n_streams, tokens_per_sample=tokens_per_sample)
     if nb == 0:
         raise ValueError("no workspace size for these arguments (more than 32 modulation rows?)")
-    return torch.empty((nb,), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty((nb,), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def _strategy(strategy) -> int:

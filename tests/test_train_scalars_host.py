@@ -1,4 +1,5 @@
-"""Host-side checks of an AdamW step's scalars (no GPU: each call is refused, at last for want of a plan)."""
+"""Host-side checks of an AdamW step's scalars (no GPU: each call is refused, at last for want of a plan), and of
+where workspaces lie."""
 from __future__ import annotations
 
 import ctypes
@@ -32,4 +33,5 @@ def test_a_workspace_lies_on_the_device_asked_for(L, monkeypatch, device, want):
     asked = []
     monkeypatch.setattr(train.torch, "empty", lambda *a, device, **kw: asked.append(device))
     train.ffn_workspace(4, 64, 64, device=device)
-    assert asked == [want] and type(asked[0]) is type(want)
+    sol.adaln_workspace(4, 256, 256, device=device)
+    assert asked == [want] * 2 and all(type(a) is type(want) for a in asked)
