@@ -3,10 +3,11 @@
 //
 // Per value 8 bytes of parameter, 2 or 4 of gradient, 16 of f32 (4 of 8-bit) moments and 2 of a
 // bf16 copy.  One CTA takes one chunk of 4096 values of one tensor, found through a table that
-// the plan holds.  With f32 moments HBM bounds the step (212 M values with norm and bf16 copy:
-// 1.008 ms, 6.7 TB/s of the bytes that move), and with 8-bit moments too (0.56 ms, 6.8 TB/s), as long as
-// eight CTAs of four warps hide the latencies of its 77 instructions a value (the codes, the
-// roots, the random rounding).
+// the plan holds.  212 M values, bf16 gradients and copies: with f32 moments 28 bytes a value in 914 us,
+// 6.5 TB/s, the rate of a plain copy (with the norm, which reads the gradients once more: 30 bytes,
+// 0.99 ms); with 8-bit moments 16.06 bytes in 558 us, 6.1 TB/s (with the norm 0.64 to 0.72 ms), as long as eight CTAs of
+// four warps an SM hide the latencies of its 77 instructions a value (the codes, the roots, the random
+// rounding): that is what keeps it 7% from a copy.
 #include <algorithm>
 #include <cmath>
 
@@ -405,7 +406,7 @@ __device__ __forceinline__ void load4s(const bf16* p, float2* f)
 
 // A warp takes one block of 256 values at a time, eight a lane, two blocks in flight.  A CTA is small
 // so that its warps need not wait for each other's end, and is done after two blocks a warp, so that reads and
-// writes stay close together in memory.  212 M values, bf16 gradients and copies: 559 us = 6.8 TB/s (a lane on
+// writes stay close together in memory.  212 M values, bf16 gradients and copies: 558 us = 6.1 TB/s (a lane on
 // eight values in a row, CTAs of 256 threads: 718, of 128: 679; four blocks a warp instead of two: 984).
 template <typename G, bool ROOT_FTZ>
 __global__ void __launch_bounds__(STEP8_THREADS, STEP8_CTAS) k_step8(const AdamwTable t, const __grid_constant__ Scalars h)
@@ -691,7 +692,7 @@ cudaError_t launch_adamw_step(const AdamwTable& t, sol_dtype grad_dt, int state_
     h.grad_factor = a.grad_factor;
     // The powers of a step counted on the device: in each CTA where all run at once, which costs 1 us and the
     // launch of k_count 5 (20,000 values, 8 bits: 7.9 against 13.2 us a call); else k_count, once for all (212 M
-    // values: 573 against 626 us, 558 with the host's step).
+    // values: 573 to 597 against 626 us, 558 with the host's step).
     const bool counted = a.step_device && t.n_chunks > 148 * 3;
     if (counted) {
         h.count = t.count;

@@ -16,9 +16,10 @@
 // loading half of A and half of B) on 256 x 256 or 512 x 256; plan() takes the one whose estimated
 // time is least.
 //
-// At d 5120, width 13,824 and 31,248 tokens: forward with u kept 10.2 ms (1.30 PFLOP/s), backward
-// 21.5 ms (1.23), both at the power cap, where cuBLAS alone reaches 1.38; at 1,252 tokens 0.48 and
-// 0.97 ms; few tokens of small blocks go to k_ffn_small.cu.
+// At d 5120, width 13,824 and 31,248 tokens: forward with u kept 10.0 to 10.5 ms (1.32 to 1.26 PFLOP/s), backward
+// 21.4 to 23.0 ms (1.24 to 1.15), both at the power cap, where cuBLAS alone reaches 1.38; at 1,252 tokens 0.48
+// and 0.98 ms; few tokens of small blocks go to k_ffn_small.cu.  Weight gradients in f32, or added to what
+// is there, leave by the slower way that finish16 describes.
 // Everything outside a tensor is read as zero by the tensor copies (ragged M, N and K) and
 // never stored.
 //
@@ -429,7 +430,8 @@ __device__ void run_mma(const Params& p, uint8_t* ring, Bars* b, const Where& w)
 
 // ---------------------------------------------------------------------------------
 // The activation and its gradient, in fp32 with one ex2 and one reciprocal on the MUFU
-// pipe (relative error a few 1e-7, far below half a bf16 step).
+// pipe.  Relative error a few 1e-7, and |a| * 6e-8 from rounding the argument of ex2: at most some
+// 1e-5 before the sigmoid of a negative a vanishes, far below half a bf16 step (2e-3).
 
 __device__ __forceinline__ float sigmoid_fast(float a)
 {
@@ -488,6 +490,11 @@ __device__ __forceinline__ void get16(const bf16* src, uint4& lo, uint4& hi, int
 
 // The epilogue of 16 columns of one row, the first n of them inside the output.  STORE: v is
 // the product.  UP: v and g are a and b.  DACT: v is d_act, ua and ub hold a and b.
+//
+// It ends k_join's tiles, and the whole tiles of gradients in f32 or added to what is there, straight from
+// registers: 16 or 32 bytes a lane into 32 rows, on a 512 x 256 tile with nothing to hide it.  Backward pass at d 5120,
+// width 13,824, us: 1,252 tokens bf16 set (through shared memory) 860, bf16 added 1,100, f32 set 1,140, f32 added 2,400;
+// 31,248 tokens 21,800, 22,100, 22,000, 24,800.
 template <int MODE>
 __device__ __forceinline__ void finish16(const Params& q, const Product& p, int64_t row, int32_t col, int n, float* v, const float* g,
                                          const uint4* ua, const uint4* ub)
@@ -980,7 +987,7 @@ bool out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t width, int64_t
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The maps of a product's epilogue; a single row's stride counts as its width.
+// The maps of a product's epilogue.
 bool out_maps(ffn::Maps& m, int i, const FfnProduct& g)
 {
     auto one = [&](CUtensorMap* t, const void* p, int64_t ld, int32_t cols) {

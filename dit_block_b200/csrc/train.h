@@ -47,16 +47,18 @@ size_t ffn_slot_bytes(int64_t rows);
 cudaError_t launch_ffn_products(FfnProduct* g, int n, bool after, cudaStream_t s);
 
 // The whole forward pass for a few tokens (k_ffn_small.cu).  Measured against k_ffn.cu, us, u kept:
-//     tokens      1           16          32          64          96          128         300
-//     64 x 64     3.2 : 8.2   3.8 : 8.3   4.7 : 8.4   4.8 : 8.6   5.0 : 8.8   4.9 : 9.1   5.0 : 8.7
-//     256 x 512   3.4 : 10.4  4.6 : 10.5  5.7 : 10.5  6.1 : 10.7  7.8 : 11.0  8.1 : 11.3  15.5 : 11.7
-//     568 x 936   3.9 : 14.0  5.4 : 14.1  7.0 : 14.1  9.6 : 15.0  11.7 : 16.3 14.1 : 17.8 29.7 : 18.2
-//     1000 x 2504 6.4 : 18.0  9.4 : 18.2  12.9 : 18.3 16.6 : 20.0 24.7 : 21.8 28.9 : 23.2
-//     3000 x 4000 18.1 : 28.7 26.3 : 29.0 31.8 : 29.6 57.5 : 31.1
+//     tokens      1           16          32          64          96          128         160         192         300
+//     64 x 64     3.2 : 8.2   3.8 : 8.3   4.7 : 8.4   4.8 : 8.6   5.0 : 8.8   4.9 : 9.1   5.0 : 8.7   5.0 : 8.7   5.0 : 8.7
+//     256 x 512   3.4 : 10.4  4.6 : 10.5  5.7 : 10.5  6.1 : 10.7  7.8 : 11.0  8.1 : 11.3  9.9 : 11.5  10.4 : 11.5 15.5 : 11.7
+//     568 x 936   3.9 : 14.0  5.4 : 14.1  7.0 : 14.1  9.6 : 15.0  11.7 : 16.3 14.1 : 17.8 17.4 : 18.1 19.9 : 18.1 29.7 : 18.2
+//     1000 x 2504 6.4 : 18.0  9.4 : 18.2  12.9 : 18.3 16.6 : 20.0 24.7 : 21.8 28.9 : 23.2 36.8 : 22.6 42.0 : 22.6
+//     3000 x 4000 18.1 : 28.7 26.3 : 29.0 31.8 : 29.6 57.5 : 31.1 -           94 : 38     117 : 41
 //     5120 x 13824 70 : 87    101 : 87    141 : 88
 // k_ffn.cu takes 8 to 14 us beside its k-blocks and the weights' bytes at 6.2 TB/s; this one 3 us, with 6 TB/s
 // for up to 8 tokens, and less the more of them, whose values cost as many loads as the weights.  Long rows of
-// W_down are few CTAs' work: 200 x 13000 takes 20.0 : 20.9 with 32 tokens, 33.5 : 23.6 with 64.
+// W_down are few CTAs' work: 200 x 13000 takes 20.0 : 20.9 with 32 tokens, 33.5 : 23.6 with 64.  The rule has no
+// budget between the one up to 128 tokens and the one of the smallest blocks, which leaves 256 x 512 from 129 to some 200
+// tokens, and 568 x 936 to some 165, to k_ffn.cu: 1 to 3 us more than here.
 inline bool ffn_small_fits(int64_t T, int64_t d, int64_t inner)
 {
     if (T <= 8) return true;
@@ -73,14 +75,16 @@ struct FfnSmall {
 cudaError_t launch_ffn_small(const FfnSmall& f, cudaStream_t s);
 
 // The whole backward pass for a few tokens (k_ffn_small.cu), in two launches.  Measured as above, all gradients:
-//     tokens      1           16          32          64          96          128         200
-//     64 x 64     4.0 : 10.5  4.5 : 10.3  5.7 : 10.3  6.7 : 10.4  7.5 : 10.5  8.8 : 10.8  10.5 : 10.7
-//     256 x 512   5.1 : 15.9  6.1 : 15.8  8.1 : 15.8  8.5 : 16.0  10.0 : 16.4 11.5 : 17.0 13.3 : 16.9
-//     568 x 936   7.5 : 22.4  8.6 : 22.6  11.0 : 22.8 12.4 : 23.3 13.6 : 22.7 15.7 : 23.9 18.9 : 24.2
+//     tokens      1           16          32          64          96          128         200         256         300
+//     64 x 64     4.0 : 10.5  4.5 : 10.3  5.7 : 10.3  6.7 : 10.4  7.5 : 10.5  8.8 : 10.8  10.5 : 10.7 11.8 : 10.9 13.8 : 11.2
+//     256 x 512   5.1 : 15.9  6.1 : 15.8  8.1 : 15.8  8.5 : 16.0  10.0 : 16.4 11.5 : 17.0 13.3 : 16.9 17.6 : 17.3 20.6 : 17.2
+//     568 x 936   7.5 : 22.4  8.6 : 22.6  11.0 : 22.8 12.4 : 23.3 13.6 : 22.7 15.7 : 23.9 18.9 : 24.2 22.7 : 25.0 25.3 : 25.7
 //     1000 x 2504 13.3 : 38.5 14.8 : 38.6 19.1 : 38.7 25.3 : 39.2 30.9 : 33.7 35.9 : 35.2 53.2 : 37.5
 //     640 x 8800  20.8 : 56.8 25.0 : 57.0 33.3 : 57.2 50.9 : 57.9 91.5 : 46.8
 //     3000 x 4000 44 : 94     48 : 93     59 : 94     84 : 96     123 : 74
 //     5120 x 13824 181 : 288  214 : 290   293 : 291   464 : 292
+// The rule's ends leave 568 x 936 past 224 tokens and 1000 x 2504 from 80 to some 125 to k_ffn.cu: up to 2 and 3 us more
+// than here.
 inline bool ffn_small_backward_fits(int64_t T, int64_t d, int64_t inner)
 {
     if (T <= 16) return d * inner < (int64_t)1 << 40;  // tiles of the gradients below 2^31

@@ -68,8 +68,8 @@ class FeedForward:
         return train.ffn(y, x, *self.weights, workspace=self.workspace)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """y for x [n, d], n <= max_tokens; keeps x and the pre-activation for backward.  y lies in this object's
-        buffer, which the next call writes."""
+        """y for x [n, d], n <= max_tokens; keeps the pre-activation, and x itself (no copy, so it must stay as it is),
+        for backward.  y lies in this object's buffer, which the next forward or infer writes."""
         n = x.shape[0]
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens are more than max_tokens ({self.max_tokens})")
@@ -87,7 +87,8 @@ class FeedForward:
         return self.dx[:n]
 
     def update(self, max_norm: float = float("inf")) -> None:
-        """One AdamW step at the learning rate ``self.lr`` holds, gradients clipped to a norm of max_norm."""
+        """One AdamW step at the learning rate ``self.lr`` holds, this block's gradients clipped to a norm of max_norm
+        (infinite: not clipped; ``self.norm`` is measured all the same)."""
         self.optimizer.grad_norm(self.norm, max_norm, workspace=self.norm_workspace)
         self.step.add_(1)
         try:

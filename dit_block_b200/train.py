@@ -205,7 +205,8 @@ def _flat(name, t, n, dtype, device: int):
 
 
 class AdamW:
-    """A plan of AdamW steps over many tensors (sol_adamw_plan_create), which holds the tensors.
+    """A plan of AdamW steps over many tensors (sol_adamw_plan_create), which holds the tensors: each step reads
+    these gradients, written anew.
 
     params f32, grads all f32 or all bf16, m and v f32, or int8 and uint8 with one f32 scale a block of
     256 values in m_scales / v_scales (zeros to begin with); copies: bf16 tensors (or None for
@@ -261,7 +262,8 @@ class AdamW:
         return torch.empty(NORM_WORKSPACE, dtype=torch.uint8, device=self.device)
 
     def grad_norm(self, out, max_norm, *, workspace, stream=None):
-        """out[0] = norm of all gradients, out[1] = min(1, max_norm / (out[0] + 1e-6))  (sol_adamw_grad_norm)."""
+        """out[0] = norm of all gradients, out[1] = min(1, max_norm / (out[0] + 1e-6)), 1 for any norm but NaN where
+        max_norm is infinite  (sol_adamw_grad_norm)."""
         dev = self._index
         _call("sol_adamw_grad_norm", dev, stream, _flat("out", out, 2, torch.float32, dev), self._handle, max_norm,
               *_space(workspace, dev))

@@ -144,7 +144,10 @@ typedef struct {
 
 /* A plan holds the tensors' addresses on the current device (one allocation, made here, not inside a
  * stream capture, and freed by destroy, which may meet a capture that does not use the plan; a captured
- * graph that uses it must not outlive it).  `tensors` is a host array, copied.  Every pointer is 16-byte aligned (scales: 4); no written buffer may overlap another
+ * graph that uses it must not outlive it).  `tensors` is a host array, copied: every buffer, the gradients'
+ * too, stays where it is as long as the plan is used, so that gradients are written again at each step, not
+ * allocated again (making a plan takes an allocation, two copies and a wait for them, more than a
+ * small step).  Every pointer is 16-byte aligned (scales: 4); no written buffer may overlap another
  * buffer of the plan.  grad_dt: SOL_DTYPE_F32 or SOL_DTYPE_BF16, of all gradients. */
 typedef struct sol_adamw_plan sol_adamw_plan;
 sol_status sol_adamw_plan_create(sol_adamw_plan** plan, const sol_adamw_tensor* tensors, int32_t n_tensors,
